@@ -2,13 +2,14 @@
 
 Argument marshalling only: every function below checks tensor dtypes/devices,
 takes device pointers and torch's current stream, and calls the C entry point of
-the same name declared in include/qmv.h. All computation happens in the HIP
+the same name declared in include/qmv.h or include/qmm_fp8.h. All computation happens in the HIP
 kernels of the library; there is no fallback path. Importing this package
 without a built library raises ImportError.
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -23,6 +24,8 @@ __all__ = [
     "qmv_dequant_q4_0_f32", "qmv_stream_read", "q4_0_bytes",
     "q4_k_bytes", "q5_k_bytes", "q6_k_bytes", "q8_0_bytes",
     "iq4_xs_bytes", "EXPORTS",
+    "qmm_fp8_quant", "qmm_fp8_quant_silu_mul", "qmm_fp8", "qmm_fp8_workspace", "qmm_fp8_grouped", "qmm_bf16_grouped",
+    "FP8_EXPORTS",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqmv.so")
@@ -64,6 +67,18 @@ EXPORTS = {
     "qmv_stream_read": (_c_int, [_vp, _c_size, _vp, _c_int, _c_int, _c_int, _vp]),
 }
 
+# name -> (restype, argtypes); mirrors include/qmm_fp8.h
+FP8_EXPORTS = {
+    "qmm_fp8_quant": (_c_int, [_vp, _c_int, _vp, _vp, _c_int, _c_int, _vp]),
+    "qmm_fp8_quant_silu_mul": (_c_int, [_vp, _c_int, _vp, _vp, _c_int, _c_int, _vp]),
+    "qmm_fp8_workspace": (_c_size, [_c_int, _c_int, _c_int, _c_int]),
+    "qmm_fp8": (_c_int, [_vp, _c_size, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp, _c_size, _vp]),
+    "qmm_fp8_grouped": (_c_int, [_vp, _c_size, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                 _c_int, _vp]),
+    "qmm_bf16_grouped": (_c_int, [_vp, _c_size, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                  _vp]),
+}
+
 
 def _load():
     # torch's HIP build ships its own libamdhip64 (same soname as the system one).
@@ -77,7 +92,7 @@ def _load():
             f"{LIB_PATH} is not built; run `python gguf_block_quantized_qmv_amd/build.py` "
             "(or __graft_entry__.build()) first")
     handle = ctypes.CDLL(LIB_PATH)
-    for name, (res, args) in EXPORTS.items():
+    for name, (res, args) in (*EXPORTS.items(), *FP8_EXPORTS.items()):
         fn = getattr(handle, name)
         fn.restype = res
         fn.argtypes = args
@@ -455,3 +470,175 @@ def qmv_stream_read(buf, grid: int = 1024, depth: int = 4, nontemporal: bool = F
     _check(lib.qmv_stream_read(_ptr(buf), _nbytes(buf), _ptr(sink), grid, depth, int(nontemporal), _stream(stream)),
            "qmv_stream_read")
     return sink
+
+
+# ---------------------------------------------------------------- e4m3 and grouped products
+
+def _blocks(k: int) -> int:
+    return -(-k // 128)
+
+
+def _e4m3_types():
+    torch = _torch()
+    return (torch.float8_e4m3fn, torch.uint8)
+
+
+def _float_type(t, name):
+    torch = _torch()
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError(f"{name} has dtype {t.dtype}, expected float32 or bfloat16")
+    return 0 if t.dtype == torch.float32 else 1   # QMM_F32, QMM_BF16
+
+
+def _same_device(named):
+    first_name, first = named[0]
+    for name, t in named[1:]:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, {first_name} on {first.device}")
+
+
+def _shape(t, name, *shape):
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+
+
+def _on(device, stream):
+    """Makes the tensors' own device current for the C call; its current stream unless one is given."""
+    torch = _torch()
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    if s.device != device:
+        raise ValueError(f"stream is on {s.device}, the tensors on {device}")
+    same = torch.cuda.current_device() == device.index
+    return contextlib.nullcontext() if same else torch.cuda.device(device), ctypes.c_void_p(s.cuda_stream)
+
+
+def _quant(fn, name, x, gated, xq, xs, stream):
+    torch = _torch()
+    _dev(x, "x", (torch.float32, torch.bfloat16))
+    if x.dim() != 2 or (gated and x.shape[1] % 2):
+        raise ValueError(f"{name}: x must be [m, {'2 k' if gated else 'k'}], got {tuple(x.shape)}")
+    m, k = x.shape[0], x.shape[1] // (2 if gated else 1)
+    if xq is None:
+        xq = torch.empty((m, k), dtype=torch.float8_e4m3fn, device=x.device)
+    if xs is None:
+        xs = torch.empty((_blocks(k), m), dtype=torch.float32, device=x.device)
+    _shape(_dev(xq, "xq", _e4m3_types()), "xq", m, k)
+    _shape(_dev(xs, "xs", (torch.float32,)), "xs", _blocks(k), m)
+    _same_device([("x", x), ("xq", xq), ("xs", xs)])
+    guard, s = _on(x.device, stream)
+    with guard:
+        _check(fn(_ptr(x), _float_type(x, "x"), _ptr(xq), _ptr(xs), m, k, s), name)
+    return xq, xs
+
+
+def qmm_fp8_quant(x, xq=None, xs=None, stream=None):
+    """Rows x [m, k] (fp32 or bf16) as e4m3 codes xq [m, k] with fp32 scales xs [ceil(k/128), m]; returns (xq, xs)."""
+    return _quant(lib.qmm_fp8_quant, "qmm_fp8_quant", x, False, xq, xs, stream)
+
+
+def qmm_fp8_quant_silu_mul(x, xq=None, xs=None, stream=None):
+    """As qmm_fp8_quant on silu(gate) * up [m, k], where x [m, 2 k] holds a row's gate values and then its up values."""
+    return _quant(lib.qmm_fp8_quant_silu_mul, "qmm_fp8_quant_silu_mul", x, True, xq, xs, stream)
+
+
+def qmm_fp8_workspace(m: int, n: int, k: int, out_dtype=None) -> int:
+    """Bytes of ws a qmm_fp8 call of this shape needs (y fp32 unless out_dtype says bf16)."""
+    torch = _torch()
+    return lib.qmm_fp8_workspace(m, n, k, 0 if out_dtype in (None, torch.float32) else 1)
+
+
+def _y(y, rows, n, out_dtype, device):
+    torch = _torch()
+    if y is None:
+        y = torch.empty((rows, n), dtype=out_dtype or torch.float32, device=device)
+    if out_dtype is not None and y.dtype != out_dtype:
+        raise TypeError(f"y has dtype {y.dtype}, out_dtype is {out_dtype}")
+    _shape(_dev(y, "y", None), "y", rows, n)
+    return y, _float_type(y, "y")
+
+
+def qmm_fp8(w, w_scale, x, x_scale, n: int, k: int, y=None, out_dtype=None, ws=None, stream=None):
+    """y[m, n] = x @ w^T for e4m3 w [n, k] and x [m, k] with scales w_scale [ceil(n/128), ceil(k/128)] and
+    x_scale [ceil(k/128), m] (as qmm_fp8_quant gives them); y is fp32 unless y or out_dtype says bf16.
+
+    ws: None allocates the workspace the shape needs (if any), or a uint8 device
+    tensor of at least qmm_fp8_workspace(m, n, k, y.dtype) bytes to reuse.
+    """
+    torch = _torch()
+    _shape(_dev(w, "w", _e4m3_types()), "w", n, k)
+    _shape(_dev(w_scale, "w_scale", (torch.float32,)), "w_scale", _blocks(n), _blocks(k))
+    _dev(x, "x", _e4m3_types())
+    m = x.shape[0]
+    _shape(x, "x", m, k)
+    _shape(_dev(x_scale, "x_scale", (torch.float32,)), "x_scale", _blocks(k), m)
+    y, y_type = _y(y, m, n, out_dtype, x.device)
+    guard, s = _on(x.device, stream)
+    with guard:
+        if ws is None:
+            need = lib.qmm_fp8_workspace(m, n, k, y_type)
+            if need:
+                with torch.cuda.stream(stream):
+                    ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+        else:
+            _dev(ws, "ws", (torch.uint8,))
+        _same_device([("x", x), ("w", w), ("w_scale", w_scale), ("x_scale", x_scale), ("y", y), ("ws", ws)])
+        _check(lib.qmm_fp8(_ptr(w), _nbytes(w), _ptr(w_scale), _ptr(x), _ptr(x_scale), _ptr(y), y_type, m, n, k,
+                           _ptr(ws), _nbytes(ws), s), "qmm_fp8")
+    return y
+
+
+def _grouped(name, w, w_scale, x, x_scale, offsets, n, k, row_index, y, out_dtype, stream):
+    torch = _torch()
+    fp8 = w_scale is not None
+    types = _e4m3_types() if fp8 else _bf16_types()
+    _dev(w, "w", types)
+    e = w.shape[0]
+    _shape(w, "w", e, n, k)
+    _dev(x, "x", types)
+    x_rows = x.shape[0]
+    _shape(x, "x", x_rows, k)
+    if fp8:
+        _shape(_dev(w_scale, "w_scale", (torch.float32,)), "w_scale", e, _blocks(n), _blocks(k))
+        _shape(_dev(x_scale, "x_scale", (torch.float32,)), "x_scale", _blocks(k), x_rows)
+    _shape(_dev(offsets, "offsets", (torch.int32,)), "offsets", e + 1)
+    rows = x_rows
+    if row_index is not None:
+        rows = row_index.numel()
+        _shape(_dev(row_index, "row_index", (torch.int32,)), "row_index", rows)
+    if y is None:
+        # rows that belong to no expert are not written: zeros there rather than what the memory held
+        with torch.cuda.stream(stream):
+            y = torch.zeros((rows, n), dtype=out_dtype or torch.float32, device=x.device)
+    y, y_type = _y(y, rows, n, out_dtype, x.device)
+    if rows == 0:
+        return y
+    _same_device([("x", x), ("w", w), ("w_scale", w_scale), ("x_scale", x_scale), ("offsets", offsets),
+                  ("row_index", row_index), ("y", y)])
+    guard, s = _on(x.device, stream)
+    with guard:
+        if fp8:
+            rc = lib.qmm_fp8_grouped(_ptr(w), _nbytes(w), _ptr(w_scale), _ptr(x), _ptr(x_scale), _ptr(offsets),
+                                     _ptr(row_index), _ptr(y), y_type, rows, x_rows, n, k, e, s)
+        else:
+            rc = lib.qmm_bf16_grouped(_ptr(w), _nbytes(w), _ptr(x), _ptr(offsets), _ptr(row_index), _ptr(y), y_type,
+                                      rows, x_rows, n, k, e, s)
+    _check(rc, name)
+    return y
+
+
+def qmm_fp8_grouped(w, w_scale, x, x_scale, offsets, n: int, k: int, row_index=None, y=None, out_dtype=None,
+                    stream=None):
+    """Rows offsets[e] .. offsets[e+1] - 1 of y [rows, n] = x rows @ w[e]^T for e4m3 w [experts, n, k] and x, scales as
+    in qmm_fp8 with one more leading dimension for w_scale; offsets int32 [experts + 1] on the device.
+
+    row_index (int32, one per row of y): the row of x to take, outside x for a row of zeros; None: the same row.
+    Rows of y that belong to no expert are left as they were (zeros when y is None).
+    """
+    if w_scale is None:
+        raise TypeError("w_scale must be a torch tensor")
+    return _grouped("qmm_fp8_grouped", w, w_scale, x, x_scale, offsets, n, k, row_index, y, out_dtype, stream)
+
+
+def qmm_bf16_grouped(w, x, offsets, n: int, k: int, row_index=None, y=None, out_dtype=None, stream=None):
+    """As qmm_fp8_grouped on bf16 w [experts, n, k] and x [x_rows, k]."""
+    return _grouped("qmm_bf16_grouped", w, None, x, None, offsets, n, k, row_index, y, out_dtype, stream)

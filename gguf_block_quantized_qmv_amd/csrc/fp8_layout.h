@@ -1,0 +1,97 @@
+// Sizes and launch plans of the e4m3 and grouped products (include/qmm_fp8.h).
+// Plain C++ with no HIP dependency: the argument checks (fp8_api.cpp, built
+// with g++) and the kernel files use the same arithmetic. Everything depends on
+// the arguments only, never on the device, so a call's numerical program is
+// fixed by its shape.
+#pragma once
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "../../include/qmm_fp8.h"
+
+namespace qmv {
+namespace fp8 {
+
+constexpr int kBlock = 128;   // values of k under one scale
+constexpr int kSlots = 256;   // compute units a plan fills (a 256-CU MI355X)
+
+constexpr int blocks_of(int k) { return (k + kBlock - 1) / kBlock; }
+constexpr int ceil_div(int a, int b) { return (a + b - 1) / b; }
+
+// ---- tile shapes (rows of x by rows of w of one workgroup) -------------------
+
+enum Tile { kTile32 = 0, kTile64 = 1, kTile128 = 2, kTile256 = 3 };
+constexpr int tile_rows(int t) { return t == kTile32 ? 32 : t == kTile64 ? 64 : t == kTile128 ? 128 : 256; }
+constexpr int tile_cols(int t) { return t == kTile256 ? 256 : 128; }
+
+// ---- dense -------------------------------------------------------------------
+
+struct DensePlan {
+  bool stream;   // the weight-streaming kernel (m <= QMM_SAME_ROWS), no workspace
+  int tile;      // else a Tile
+  int splits;    // parts of k, summed by a second launch when more than one
+};
+
+// Waves of a streaming workgroup: each takes every waves-th block of 128.
+constexpr int stream_waves(int nb) { return nb >= 64 ? 16 : nb >= 16 ? 8 : 4; }
+
+inline DensePlan dense_plan(int m, int n, int k, bool y_bf16) {
+  DensePlan p{m <= QMM_SAME_ROWS, kTile128, 1};
+  if (p.stream) return p;
+  p.tile = m <= 32 ? kTile32 : m <= 64 ? kTile64 : kTile128;
+  const int64_t big = (int64_t)ceil_div(m, 256) * ceil_div(n, 256);
+  if (y_bf16 && m > 128 && big >= kSlots) p.tile = kTile256;
+  const int64_t tiles = (int64_t)ceil_div(m, tile_rows(p.tile)) * ceil_div(n, tile_cols(p.tile));
+  const int nb = blocks_of(k);
+  if (tiles < 2 * kSlots && p.tile != kTile256) {
+    int64_t s = 2 * kSlots / tiles;
+    if (s > nb / 4) s = nb / 4;      // at least four blocks a part
+    if (s > 16) s = 16;
+    p.splits = s < 1 ? 1 : (int)s;
+  }
+  return p;
+}
+
+inline size_t dense_workspace(int m, int n, int k, bool y_bf16) {
+  const DensePlan p = dense_plan(m, n, k, y_bf16);
+  return p.splits > 1 ? (size_t)p.splits * (size_t)m * (size_t)n * 4 : 0;
+}
+
+// ---- grouped -----------------------------------------------------------------
+
+// Expected rows of an expert that has any: host code cannot see the offsets, so
+// the tile goes by rows spread evenly.
+struct GroupedPlan {
+  bool stream;
+  int tile;
+};
+
+inline GroupedPlan grouped_plan(int rows, int n_experts) {
+  const int avg = rows / (n_experts < 1 ? 1 : n_experts);
+  GroupedPlan p{avg <= 4, kTile32};
+  p.tile = avg <= 32 ? kTile32 : avg <= 64 ? kTile64 : kTile128;
+  return p;
+}
+
+// Row tiles a grouped launch can need: every expert with rows may have one
+// partial tile.
+inline int64_t grouped_row_tiles(int rows, int n_experts, int bm) {
+  return (int64_t)rows / bm + (rows < n_experts ? rows : n_experts);
+}
+
+// Workgroups of a launch: 2^22 of up to 512 threads keep a grid inside 32 bits.
+constexpr int64_t kMaxWorkgroups = (int64_t)1 << 22;
+
+inline bool dense_fits_grid(int m, int n, int k, bool y_bf16) {
+  const DensePlan p = dense_plan(m, n, k, y_bf16);
+  return p.stream || (int64_t)ceil_div(m, tile_rows(p.tile)) * ceil_div(n, tile_cols(p.tile)) * p.splits <= kMaxWorkgroups;
+}
+
+inline bool grouped_fits_grid(int rows, int n, int n_experts) {
+  const GroupedPlan p = grouped_plan(rows, n_experts);
+  return p.stream || grouped_row_tiles(rows, n_experts, tile_rows(p.tile)) * ceil_div(n, tile_cols(p.tile)) <= kMaxWorkgroups;
+}
+
+}  // namespace fp8
+}  // namespace qmv

@@ -1,0 +1,548 @@
+// Products of e4m3 rows with block-scaled e4m3 weights, dense and grouped by
+// expert, and the grouped product on bf16; gfx950 matrix cores.
+//
+// Along k everything is counted in blocks of 128 bytes: 128 e4m3 values under
+// one scale, or 64 bf16 values. The weights are the A operand (16 rows of w),
+// the activations the B operand (16 rows of x), so a lane's four results are
+// four neighbouring columns of one row of y. An MFMA takes k in any order as
+// long as both operands agree: lane l of a fragment holds the 16-byte chunks
+// l / 16 and l / 16 + 4 of row l % 16.
+//
+// e4m3: the scales vary from block to block, so a block's product starts from
+// zero and enters the sum by one fma per result, y += (xs * ws) * d, in fp32.
+// Two ways to a block's product:
+//  * kNative, one v_mfma_f32_16x16x128_f8f6f4. The instruction aligns each
+//    eight neighbouring products to the largest of them and cuts what lies 13
+//    bits below (measured: 2^16 + 2^2 in one group of eight gives 2^16, in two
+//    groups 2^16 + 2^2); on normal data that is 1.6e-5 of the result's norm.
+//  * kExact, the codes as bf16 (exact, two by one v_cvt_scalef32_pk_bf16_fp8)
+//    through four v_mfma_f32_16x16x32_bf16, whose sums keep fp32 (5e-8), at
+//    half the matrix rate.
+// Results in fp32 are kExact. Results in bf16, whose rounding (2^-9 on average
+// of its value) is a hundred times the native sums' error, are kNative where
+// the matrix cores bound the product and kExact where the weight stream does.
+// bf16 operands (kBf16) take two v_mfma_f32_16x16x32_bf16 a block.
+#include "fp8_internal.h"
+#include "fp8_layout.h"
+#include "qmv_device.h"
+#include "../../include/qmm_fp8.h"
+
+namespace qmv {
+namespace {
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+// One block's chunk pair of one lane.
+struct Frag {
+  v4i lo, hi;
+};
+
+enum Kind { kNative, kExact, kBf16 };
+constexpr bool is_e4m3(Kind kind) { return kind != kBf16; }
+
+// Sixteen e4m3 codes as two bf16 MFMA operands (exact; NaN stays NaN).
+__device__ __forceinline__ void widen(const v4i c, bf16x8 &lo, bf16x8 &hi) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)c[i], 1.0f, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)c[i], 1.0f, true);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)c[2 + i], 1.0f, false);
+    const bf16x2 e = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)c[2 + i], 1.0f, true);
+    lo[4 * i] = a[0]; lo[4 * i + 1] = a[1]; lo[4 * i + 2] = b[0]; lo[4 * i + 3] = b[1];
+    hi[4 * i] = d[0]; hi[4 * i + 1] = d[1]; hi[4 * i + 2] = e[0]; hi[4 * i + 3] = e[1];
+  }
+}
+
+// A block's operand in the form its instructions take.
+template <Kind KIND>
+struct Operand {
+  v8i v;
+  __device__ __forceinline__ void set(const Frag &f) { v = __builtin_shufflevector(f.lo, f.hi, 0, 1, 2, 3, 4, 5, 6, 7); }
+};
+template <>
+struct Operand<kExact> {
+  bf16x8 v[4];
+  __device__ __forceinline__ void set(const Frag &f) {
+    widen(f.lo, v[0], v[1]);
+    widen(f.hi, v[2], v[3]);
+  }
+};
+template <>
+struct Operand<kBf16> {
+  bf16x8 v[2];
+  __device__ __forceinline__ void set(const Frag &f) {
+    v[0] = __builtin_bit_cast(bf16x8, f.lo);
+    v[1] = __builtin_bit_cast(bf16x8, f.hi);
+  }
+};
+
+// acc += scale * (A B) over one block; scale is not used by bf16.
+template <Kind KIND>
+__device__ __forceinline__ void mma_block(const Operand<KIND> &a, const Operand<KIND> &b, const float scale, v4f &acc) {
+  if constexpr (KIND == kBf16) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[h], b.v[h], acc, 0, 0, 0);
+  } else {
+    v4f d = {0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (KIND == kNative) {
+      d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, d, 0, 0, 0, 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 4; ++h) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[h], b.v[h], d, 0, 0, 0);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(scale, d[e], acc[e]);
+  }
+}
+
+__device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
+
+// Rows of expert e, clamped to y.
+__device__ __forceinline__ void expert_rows(const int32_t *__restrict__ offsets, int e, int rows, int &begin,
+                                            int &end) {
+  begin = clampi(offsets[e], 0, rows);
+  end = clampi(offsets[e + 1], begin, rows);
+}
+
+// Row of x behind row `row` of y; false (and row 0) for an index outside x.
+__device__ __forceinline__ bool source_row(const ProductArgs &p, int row, int &src) {
+  src = p.index ? p.index[row] : row;
+  const bool ok = (unsigned)src < (unsigned)p.x_rows;
+  src = ok ? src : 0;
+  return ok;
+}
+
+__device__ __forceinline__ void store_y(const ProductArgs &p, int row, int col, float v) {
+  const size_t at = (size_t)row * p.n + col;
+  if (p.y_bf16)
+    static_cast<__bf16 *>(p.y)[at] = (__bf16)v;
+  else
+    static_cast<float *>(p.y)[at] = v;
+}
+
+// ---- a few rows: stream the weights ---------------------------------------------
+//
+// A workgroup owns 16 rows of one weight matrix and up to 16 rows of x at a
+// time; wave v takes blocks v, v + NW, ... of k straight from memory into
+// MFMA fragments (no LDS), kDepth blocks in flight, and the waves' sums are
+// added in wave order. Bound by the weight stream. The order of the sums goes
+// by (n, k) alone and the columns of an MFMA do not mix, so a row of x has the
+// same bits in any company. Grouped: workgroup (t, s) serves the s-th expert
+// that has rows, and takes 16 of its rows at a time.
+constexpr int kDepth = 4;
+
+template <Kind KIND, bool GROUPED, int NW>
+__global__ __launch_bounds__(NW * 64) void product_stream_kernel(const ProductArgs p) {
+  constexpr bool FP8 = is_e4m3(KIND);
+  __shared__ float red[NW][256];
+  const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int r = lane & 15, g = lane >> 4;
+  const int n0 = (int)blockIdx.x * 16;
+  int expert = 0, begin = 0, end = p.rows;
+  if constexpr (GROUPED) {
+    int want = (int)blockIdx.y, found = -1;
+    for (int base = 0; base < p.n_experts && found < 0; base += 64) {
+      int b0 = 0, b1 = 0;
+      if (base + lane < p.n_experts) expert_rows(p.offsets, base + lane, p.rows, b0, b1);
+      uint64_t mask = __ballot(b1 > b0);
+      const int have = __popcll(mask);
+      if (want < have) {
+        for (int i = 0; i < want; ++i) mask &= mask - 1;
+        found = base + __ffsll((unsigned long long)mask) - 1;
+      }
+      want -= have;
+    }
+    if (found < 0) return;
+    expert = __builtin_amdgcn_readfirstlane(found);
+    expert_rows(p.offsets, expert, p.rows, begin, end);
+  }
+  const int wrow = n0 + r < p.n ? n0 + r : p.n - 1;
+  const uint8_t *wp = p.w + ((size_t)expert * p.n + wrow) * p.k_bytes;
+  const float *wsp = FP8 ? p.w_scale + ((size_t)expert * fp8::ceil_div(p.n, 128) + (n0 >> 7)) * p.nb : nullptr;
+  const int count = (p.nb - wave + NW - 1) / NW;   // this wave's blocks
+
+  for (int t0 = begin; t0 < end; t0 += 16) {
+    int src;
+    source_row(p, t0 + r < end ? t0 + r : end - 1, src);
+    const uint8_t *xp = p.x + (size_t)src * p.k_bytes;
+    const float *xsp = FP8 ? p.x_scale + src : nullptr;
+
+    Frag wf[kDepth], xf[kDepth];
+    float xs[kDepth], ws[kDepth];
+    auto load = [&](int i, int u) {
+      const int b = wave + NW * (i < count ? i : count - 1);
+      const int at = b * 128 + g * 16;
+      const bool lo = at < p.k_bytes, hi = at + 64 < p.k_bytes;   // chunks past the row read as zeros
+      const v4i zero = {0, 0, 0, 0};
+      const v4i a = *reinterpret_cast<const v4i *>(wp + (lo ? at : 0));
+      const v4i c = *reinterpret_cast<const v4i *>(wp + (hi ? at + 64 : 0));
+      const v4i d = *reinterpret_cast<const v4i *>(xp + (lo ? at : 0));
+      const v4i e = *reinterpret_cast<const v4i *>(xp + (hi ? at + 64 : 0));
+      wf[u].lo = lo ? a : zero;
+      wf[u].hi = hi ? c : zero;
+      xf[u].lo = lo ? d : zero;
+      xf[u].hi = hi ? e : zero;
+      if constexpr (FP8) {
+        xs[u] = xsp[(size_t)b * p.x_rows];
+        ws[u] = wsp[b];
+      }
+    };
+    v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (count > 0) {
+#pragma unroll
+      for (int u = 0; u < kDepth; ++u) load(u, u);
+      for (int i0 = 0; i0 < count; i0 += kDepth)
+#pragma unroll
+        for (int u = 0; u < kDepth; ++u) {
+          if (i0 + u < count) {
+            Operand<KIND> a, b;
+            a.set(wf[u]);
+            b.set(xf[u]);
+            mma_block<KIND>(a, b, FP8 ? xs[u] * ws[u] : 0.0f, acc);
+          }
+          load(i0 + u + kDepth, u);
+        }
+    }
+    // lane l holds columns 4 g .. 4 g + 3 of row r of x
+    *reinterpret_cast<v4f *>(&red[wave][r * 16 + g * 4]) = acc;
+    __syncthreads();
+    if ((int)threadIdx.x < 256) {
+      const int row = t0 + ((int)threadIdx.x >> 4), col = n0 + ((int)threadIdx.x & 15);
+      float sum = red[0][threadIdx.x];
+#pragma unroll
+      for (int v = 1; v < NW; ++v) sum += red[v][threadIdx.x];
+      if (row < end && col < p.n) {
+        int at;
+        store_y(p, row, col, source_row(p, row, at) ? sum : 0.0f);
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ---- many rows: tiles through LDS --------------------------------------------------
+//
+// A workgroup owns BM rows of x by BN rows of w. Each step moves one block of
+// k of both into one of two LDS stages by direct-to-LDS loads while the waves
+// multiply the other stage; one barrier a step hands the stages over. A stage
+// row is 128 bytes, eight 16-byte chunks; chunk c of row r sits at slot
+// c ^ ((r / 2) % 8), which leaves the fragment reads (16 consecutive rows, one
+// chunk) free of bank conflicts. The direct loads write LDS in lane order, so
+// the permutation is applied to the global address each lane reads.
+constexpr int kStageRow = 128;
+
+__device__ const uint4 g_zeros[1] = {};
+
+template <int BM_, int BN_, int WM_, int WN_>
+struct Shape {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;   // waves along rows of x, of w
+  static constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
+  static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;     // MFMA tiles of a wave
+  static constexpr int kLoads = (BM + BN) / 8 / kWaves;          // 1 KiB direct loads of a wave and step
+  static constexpr int kStageBytes = (BM + BN) * kStageRow;
+  static_assert((BM + BN) % (8 * kWaves) == 0 && TM * WM * 16 == BM && TN * WN * 16 == BN, "whole tiles and loads");
+  static_assert(BN / WN <= 128 && 128 % (BN / WN) == 0, "a wave's columns lie under one weight scale");
+};
+
+__device__ __forceinline__ void load_lds16(const uint8_t *g, uint8_t *l) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)g,
+                                   (__attribute__((address_space(3))) void *)l, 16, 0, 0);
+}
+__device__ __forceinline__ void load_lds4(const float *g, float *l) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)g,
+                                   (__attribute__((address_space(3))) void *)l, 4, 0, 0);
+}
+
+// Every direct load of this wave has landed and every LDS read has returned,
+// then all waves meet.
+__device__ __forceinline__ void stage_barrier() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// id -> position in an order that gives each of the eight XCDs (workgroups are
+// dealt to them in turn) one contiguous run of [0, total).
+__device__ __forceinline__ int xcd_order(int id, int total) {
+  const int q = total >> 3, rest = total & 7, x = id & 7;
+  return x * q + (x < rest ? x : rest) + (id >> 3);
+}
+
+template <class S, Kind KIND, bool GROUPED>
+__global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const ProductArgs p) {
+  constexpr bool FP8 = is_e4m3(KIND);
+  __shared__ __attribute__((aligned(1024))) uint8_t stage0[S::kStageBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t stage1[S::kStageBytes];
+  __shared__ float scale0[FP8 ? S::BM : 64], scale1[FP8 ? S::BM : 64];
+  const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int n_tiles = fp8::ceil_div(p.n, S::BN);
+
+  // this workgroup's tile
+  int expert = 0, m0, begin = 0, end = p.rows, nt, part = 0;
+  if constexpr (GROUPED) {
+    // row tiles of each lane's run of experts, and their running sum over the lanes
+    const int per = fp8::ceil_div(p.n_experts, 64), e0 = lane * per;
+    int mine = 0;
+    for (int e = e0; e < e0 + per && e < p.n_experts; ++e) {
+      int b0, b1;
+      expert_rows(p.offsets, e, p.rows, b0, b1);
+      mine += fp8::ceil_div(b1 - b0, S::BM);
+    }
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(upto, d);
+      if (lane >= d) upto += o;
+    }
+    const int total = __builtin_amdgcn_readfirstlane(__shfl(upto, 63));
+    // decreasing offsets can give more tiles than the grid holds: they are not done
+    const int all = total < (int)gridDim.x / n_tiles ? total * n_tiles : (int)gridDim.x;
+    if ((int)blockIdx.x >= all) return;
+    const int id = xcd_order((int)blockIdx.x, all);
+    const int mt = id / n_tiles;
+    nt = id - mt * n_tiles;
+    const int owner = __ffsll((unsigned long long)__ballot(upto > mt)) - 1;
+    int left = mt - __builtin_amdgcn_readfirstlane(__shfl(upto - mine, owner));
+    expert = owner * per;
+    for (;;) {
+      expert_rows(p.offsets, expert, p.rows, begin, end);
+      const int t = fp8::ceil_div(end - begin, S::BM);
+      if (left < t) break;
+      left -= t;
+      ++expert;
+    }
+    expert = __builtin_amdgcn_readfirstlane(expert);
+    m0 = begin + left * S::BM;
+  } else {
+    const int m_tiles = fp8::ceil_div(p.rows, S::BM);
+    const int tiles = m_tiles * n_tiles;
+    int id = xcd_order((int)blockIdx.x, tiles * p.splits);
+    part = id / tiles;
+    id -= part * tiles;
+    // bands of eight row tiles, rows first within a band
+    const int band = id / (8 * n_tiles), in = id - band * 8 * n_tiles;
+    const int high = m_tiles - band * 8 < 8 ? m_tiles - band * 8 : 8;
+    nt = in / high;
+    m0 = (band * 8 + in - nt * high) * S::BM;
+  }
+  const int n0 = nt * S::BN;
+  const int blk0 = GROUPED ? 0 : (int)((int64_t)p.nb * part / p.splits);
+  const int blk1 = GROUPED ? p.nb : (int)((int64_t)p.nb * (part + 1) / p.splits);
+
+  // this lane's direct loads: row q * 8 + lane / 8 of the stage, chunk by the slot
+  const uint8_t *from[S::kLoads];
+  int chunk_at[S::kLoads];
+#pragma unroll
+  for (int i = 0; i < S::kLoads; ++i) {
+    const int row = (wave * S::kLoads + i) * 8 + (lane >> 3);
+    chunk_at[i] = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
+    if (row < S::BM) {
+      int src;
+      source_row(p, m0 + row < end ? m0 + row : end - 1, src);
+      from[i] = p.x + (size_t)src * p.k_bytes;
+    } else {
+      const int wrow = n0 + row - S::BM;
+      from[i] = p.w + ((size_t)expert * p.n + (wrow < p.n ? wrow : p.n - 1)) * p.k_bytes;
+    }
+    from[i] += chunk_at[i] + (size_t)blk0 * 128;
+  }
+  const float *scale_from = nullptr;
+  if (FP8 && wave < S::BM / 64 + (S::BM % 64 != 0)) {
+    const int row = m0 + wave * 64 + lane;
+    int src;
+    source_row(p, row < end ? row : end - 1, src);
+    scale_from = p.x_scale + src + (size_t)blk0 * p.x_rows;
+  }
+  const int tail = p.k_bytes & 127;   // bytes of a partial last block
+  auto issue = [&](int b, uint8_t *stage, float *scale) {
+    uint8_t *to = stage + wave * S::kLoads * 1024;
+    if (tail && b == p.nb - 1) {
+#pragma unroll
+      for (int i = 0; i < S::kLoads; ++i)
+        load_lds16(chunk_at[i] < tail ? from[i] : reinterpret_cast<const uint8_t *>(g_zeros), to + i * 1024);
+    } else {
+#pragma unroll
+      for (int i = 0; i < S::kLoads; ++i) {
+        load_lds16(from[i], to + i * 1024);
+        from[i] += 128;
+      }
+    }
+    if constexpr (FP8) {
+      if (S::BM % 64 == 0 ? wave < S::BM / 64 : wave == 0 && lane < S::BM) {
+        load_lds4(scale_from, scale + wave * 64);
+        scale_from += p.x_rows;
+      }
+    }
+  };
+
+  const int wm = wave / S::WN, wn = wave % S::WN;
+  const int r = lane & 15, g = lane >> 4;
+  const int frag_at = r * kStageRow + ((g ^ ((r >> 1) & 7)) << 4);   // chunk g of row r; chunk g + 4 is 64 bytes on or back
+  const int x_at = wm * S::TM * 16 * kStageRow + frag_at;
+  const int w_at = (S::BM + wn * S::TN * 16) * kStageRow + frag_at;
+  const int col0 = n0 + wn * S::TN * 16;
+  const int sblk = (col0 < p.n ? col0 : p.n - 1) >> 7;
+  const float *wsp = FP8 ? p.w_scale + ((size_t)expert * fp8::ceil_div(p.n, 128) + sblk) * p.nb : nullptr;
+
+  v4f acc[S::TM][S::TN];
+#pragma unroll
+  for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < S::TN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+
+  auto compute = [&](int b, const uint8_t *stage, const float *scale) {
+    const float ws = FP8 ? wsp[b] : 0.0f;
+    Operand<KIND> wf[S::TN];
+#pragma unroll
+    for (int j = 0; j < S::TN; ++j) {
+      Frag f;
+      f.lo = *reinterpret_cast<const v4i *>(stage + w_at + j * 2048);
+      f.hi = *reinterpret_cast<const v4i *>(stage + (w_at ^ 64) + j * 2048);
+      wf[j].set(f);
+    }
+#pragma unroll
+    for (int i = 0; i < S::TM; ++i) {
+      Frag f;
+      f.lo = *reinterpret_cast<const v4i *>(stage + x_at + i * 2048);
+      f.hi = *reinterpret_cast<const v4i *>(stage + (x_at ^ 64) + i * 2048);
+      Operand<KIND> xf;
+      xf.set(f);
+      const float s = FP8 ? scale[(wm * S::TM + i) * 16 + r] * ws : 0.0f;
+#pragma unroll
+      for (int j = 0; j < S::TN; ++j) mma_block<KIND>(wf[j], xf, s, acc[i][j]);
+    }
+  };
+
+  issue(blk0, stage0, scale0);
+  for (int b = blk0; b < blk1; b += 2) {
+    stage_barrier();
+    if (b + 1 < blk1) issue(b + 1, stage1, scale1);
+    compute(b, stage0, scale0);
+    if (b + 1 >= blk1) break;
+    stage_barrier();
+    if (b + 2 < blk1) issue(b + 2, stage0, scale0);
+    compute(b + 1, stage1, scale1);
+  }
+
+  // lane: columns 4 g .. 4 g + 3 of row r of each 16 x 16 tile
+#pragma unroll
+  for (int i = 0; i < S::TM; ++i) {
+    const int row = m0 + (wm * S::TM + i) * 16 + r;
+    if (row >= end) continue;
+    bool ok = true;
+    if constexpr (GROUPED) {
+      int src;
+      ok = source_row(p, row, src);
+    }
+#pragma unroll
+    for (int j = 0; j < S::TN; ++j) {
+      const int col = col0 + j * 16 + g * 4;
+      const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
+      const v4f v = ok ? acc[i][j] : zero;
+      if (!GROUPED && p.splits > 1) {
+        float *to = p.part + ((size_t)part * p.rows + row) * p.n + col;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (col + e < p.n) to[e] = v[e];
+        continue;
+      }
+      if ((p.n & 3) == 0) {   // four columns at once: rows of y keep the alignment of y
+        if (col >= p.n) continue;
+        const size_t at = (size_t)row * p.n + col;
+        if (p.y_bf16) {
+          typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+          *reinterpret_cast<bf16x4 *>(static_cast<__bf16 *>(p.y) + at) =
+              bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
+        } else {
+          *reinterpret_cast<v4f *>(static_cast<float *>(p.y) + at) = v;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (col + e < p.n) store_y(p, row, col + e, v[e]);
+      }
+    }
+  }
+}
+
+// y of a product split along k: the parts in the order of k.
+__global__ __launch_bounds__(256) void product_sum_kernel(const float *__restrict__ part, const ProductArgs p) {
+  const size_t count = (size_t)p.rows * p.n;
+  const size_t at = (size_t)blockIdx.x * 256 + threadIdx.x;
+  if (at >= count) return;
+  float v = part[at];
+  for (int s = 1; s < p.splits; ++s) v += part[(size_t)s * count + at];
+  if (p.y_bf16)
+    static_cast<__bf16 *>(p.y)[at] = (__bf16)v;
+  else
+    static_cast<float *>(p.y)[at] = v;
+}
+
+using Tile32 = Shape<32, 128, 1, 4>;
+using Tile64 = Shape<64, 128, 1, 4>;
+using Tile128 = Shape<128, 128, 2, 2>;
+using Tile256 = Shape<256, 256, 2, 4>;
+
+template <class S, Kind KIND, bool GROUPED>
+int launch_tile(const ProductArgs &a, unsigned grid, hipStream_t s) {
+  return launch_kernel("product_tile_kernel", product_tile_kernel<S, KIND, GROUPED>, dim3(grid), dim3(S::kThreads), 0,
+                       s, a);
+}
+
+template <Kind KIND, bool GROUPED>
+int launch_tiles(int tile, const ProductArgs &a, hipStream_t s) {
+  const int bm = fp8::tile_rows(tile), bn = fp8::tile_cols(tile);
+  const int64_t row_tiles = GROUPED ? fp8::grouped_row_tiles(a.rows, a.n_experts, bm) : fp8::ceil_div(a.rows, bm);
+  const unsigned grid = (unsigned)(row_tiles * fp8::ceil_div(a.n, bn) * a.splits);
+  switch (tile) {
+    case fp8::kTile32: return launch_tile<Tile32, KIND, GROUPED>(a, grid, s);
+    case fp8::kTile64: return launch_tile<Tile64, KIND, GROUPED>(a, grid, s);
+    case fp8::kTile128: return launch_tile<Tile128, KIND, GROUPED>(a, grid, s);
+    default:
+      if constexpr (KIND == kNative && !GROUPED) return launch_tile<Tile256, KIND, GROUPED>(a, grid, s);
+      set_error_detail("product_tile_kernel", 0, "no such tile");
+      return QMV_ERR_HIP;
+  }
+}
+
+template <Kind KIND, bool GROUPED>
+int launch_stream(const ProductArgs &a, hipStream_t s) {
+  const dim3 grid((unsigned)fp8::ceil_div(a.n, 16), GROUPED ? (unsigned)(a.rows < a.n_experts ? a.rows : a.n_experts) : 1u);
+  switch (fp8::stream_waves(a.nb)) {
+    case 16: return launch_kernel("product_stream_kernel", product_stream_kernel<KIND, GROUPED, 16>, grid, dim3(1024), 0, s, a);
+    case 8: return launch_kernel("product_stream_kernel", product_stream_kernel<KIND, GROUPED, 8>, grid, dim3(512), 0, s, a);
+    default: return launch_kernel("product_stream_kernel", product_stream_kernel<KIND, GROUPED, 4>, grid, dim3(256), 0, s, a);
+  }
+}
+
+}  // namespace
+
+int launch_fp8_dense(const ProductArgs &a, void *stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const fp8::DensePlan plan = fp8::dense_plan(a.rows, a.n, a.k_bytes, a.y_bf16);
+  if (plan.stream) return launch_stream<kExact, false>(a, s);
+  const int rc = a.y_bf16 ? launch_tiles<kNative, false>(plan.tile, a, s) : launch_tiles<kExact, false>(plan.tile, a, s);
+  if (rc || a.splits == 1) return rc;
+  const unsigned grid = (unsigned)(((size_t)a.rows * a.n + 255) / 256);
+  return launch_kernel("product_sum_kernel", product_sum_kernel, dim3(grid), dim3(256), 0, s,
+                       static_cast<const float *>(a.part), a);
+}
+
+int launch_fp8_grouped(const ProductArgs &a, void *stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const fp8::GroupedPlan plan = fp8::grouped_plan(a.rows, a.n_experts);
+  if (plan.stream) return launch_stream<kExact, true>(a, s);
+  return a.y_bf16 ? launch_tiles<kNative, true>(plan.tile, a, s) : launch_tiles<kExact, true>(plan.tile, a, s);
+}
+
+int launch_bf16_grouped(const ProductArgs &a, void *stream) {
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const fp8::GroupedPlan plan = fp8::grouped_plan(a.rows, a.n_experts);
+  return plan.stream ? launch_stream<kBf16, true>(a, s) : launch_tiles<kBf16, true>(plan.tile, a, s);
+}
+
+}  // namespace qmv

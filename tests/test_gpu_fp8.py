@@ -1,0 +1,303 @@
+"""GPU parity of the e4m3 and grouped products and of the row quantisers with the fp64 oracle.
+
+Tolerances, from the arithmetic. A product of two e4m3 (bf16) values is exact in
+fp32. A block's sum on the matrix cores adds up to 128 (64) of them, each add off
+by at most one fp32 step (2^-23 of the running magnitude, which covers
+truncation); the block enters the sum with one rounding of the scales' product
+and one of the fma, and every later block, part and wave sum adds one: fewer than
+blocks + 40 roundings. All of them act on sums no larger than A = sum |x w|, so
+|y - exact| <= (2 * 128 + blocks + 40) * 2^-24 * A. bf16 chains all k products in
+one accumulator: (2 * k + 40) * 2^-24 * A. A bf16 result adds half a step, 2^-8 of
+its value, and its blocks may come from the e4m3 instruction: that aligns each eight
+neighbouring products to the largest and cuts 13 bits below its exponent, so each of
+the other seven loses less than 2^-13 of the largest, a group less than 7 * 2^-13 of
+its magnitudes, the sum less than 7 * 2^-13 * A.
+"""
+
+import numpy as np
+import pytest
+
+from gpu_util import device, guards_intact, guarded, host
+from oracle import fp8_oracle as o
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def q():
+    import gguf_block_quantized_qmv_amd as mod
+    return mod
+
+
+@pytest.fixture(scope="module")
+def dev():
+    return device()
+
+
+def rng(*seed):
+    return np.random.default_rng(seed)
+
+
+def bf16_round(x):
+    return torch.from_numpy(np.asarray(x, dtype=np.float32)).to(torch.bfloat16)
+
+
+def codes8(g, *shape):
+    """Codes of the whole range, NaN left out, small and large magnitudes alike."""
+    c = g.integers(0, 256, shape, dtype=np.uint8)
+    return np.where((c & 127) == 127, c ^ 1, c)
+
+
+def scales(g, *shape):
+    return (2.0 ** g.uniform(-8, 2, shape)).astype(np.float32)
+
+
+def up(a, dev):
+    return torch.from_numpy(np.ascontiguousarray(a)).to(dev)
+
+
+def bound(mag, k, out, exact, bf16_inputs=False):
+    rounds = 2 * k + 40 if bf16_inputs else 2 * 128 + o.blocks(k) + 40
+    t = rounds * 2.0 ** -24 * mag
+    if out == torch.bfloat16 and not bf16_inputs:
+        t = t + 7 * 2.0 ** -13 * mag
+    return t + (2.0 ** -8 * np.abs(exact) + 2.0 ** -8 * t if out == torch.bfloat16 else 0)
+
+
+def check(got, exact, tol):
+    bad = ~(np.abs(got - exact) <= tol)
+    assert not bad.any(), (int(bad.sum()), np.argwhere(bad)[:4].tolist(),
+                           got[bad][:4].tolist(), exact[bad][:4].tolist(), tol[bad][:4].tolist())
+
+
+# ------------------------------------------------------------------ quantisers
+
+@pytest.mark.parametrize("m,k", [(1, 16), (1, 128), (3, 144), (16, 256), (17, 1040), (65, 5120), (4, 17408)])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_quant_is_the_definition_bit_for_bit(q, dev, m, k, kind):
+    g = rng(1, m, k)
+    x = (g.standard_normal((m, k)) * 10.0 ** g.uniform(-3, 3, (m, 1))).astype(np.float32)
+    x[0, : k // 2] = 0.0                                     # whole blocks of zeros when k allows
+    t = torch.from_numpy(x) if kind == "f32" else bf16_round(x)
+    sbuf_v, sbuf = guarded((o.blocks(k), m), torch.float32, dev)
+    qbuf = torch.full((m * k + 256,), 0x55, dtype=torch.uint8, device=dev)
+    xq = qbuf[128:128 + m * k].view(m, k)
+    q.qmm_fp8_quant(t.to(dev), xq=xq, xs=sbuf_v)
+    torch.cuda.synchronize()
+    assert guards_intact(sbuf) and bool((qbuf[:128] == 0x55).all()) and bool((qbuf[-128:] == 0x55).all())
+    codes, s = o.quant(t.float().numpy())
+    assert np.array_equal(host(sbuf_v), s)
+    assert np.array_equal(o.decode(host(xq)), o.decode(codes))
+
+
+def test_quant_every_border_rounds_to_even(q, dev):
+    # block maximum 448 makes the scale 1: every e4m3 value, every midpoint and its fp32 neighbours
+    v = o.VALUES[:127]
+    mids = (v[:-1] + v[1:]) / 2
+    probe = np.concatenate([v, mids, np.nextafter(mids.astype(np.float32), np.float32(0)),
+                            np.nextafter(mids.astype(np.float32), np.float32(1e9))]).astype(np.float32)
+    probe = np.concatenate([probe, -probe])
+    pad = -len(probe) % 127
+    rows = np.concatenate([probe, np.zeros(pad, np.float32)]).reshape(-1, 127)
+    x = np.concatenate([rows, np.full((len(rows), 1), 448.0, np.float32)], axis=1)
+    xq, xs = q.qmm_fp8_quant(up(x, dev))
+    assert np.array_equal(host(xs), np.ones((1, len(x)), np.float32))
+    assert np.array_equal(o.decode(host(xq.view(torch.uint8))), o.decode(o.encode(x)))
+
+
+def test_quant_tiny_huge_and_not_finite(q, dev):
+    x = np.zeros((6, 256), np.float32)
+    x[1, 3] = 1e-44                                          # a subnormal: the scale stays at 2^-126
+    x[2, 7], x[2, 8] = 3.4e38, -1e-3
+    x[3, 130] = np.inf
+    x[4, 5] = np.nan
+    x[5, :128] = 2.0 ** -126 * 448
+    xq, xs = q.qmm_fp8_quant(up(x, dev))
+    s, c = host(xs), o.decode(host(xq.view(torch.uint8)))
+    assert s[0, 0] == s[0, 1] == np.float32(2.0 ** -126) and (c[:2] == 0).all()
+    assert s[0, 2] == np.float32(np.float64(np.float32(3.4e38)) / 448) and c[2, 7] == 448 and c[2, 8] == 0
+    assert np.isinf(s[1, 3]) and s[0, 3] == np.float32(2.0 ** -126)   # the other block of the row is untouched
+    assert np.isnan(s[0, 4]) and s[1, 4] == np.float32(2.0 ** -126)
+    assert s[0, 5] == np.float32(2.0 ** -126) and (c[5, :128] == 448).all()
+    # the products of those rows, and of no others, are not finite
+    w = up(codes8(rng(9), 20, 256), dev)
+    y = host(q.qmm_fp8(w, torch.ones(1, 2, device=dev), xq, xs, 20, 256))
+    assert np.isfinite(y[[0, 1, 5]]).all() and not np.isfinite(y[[3, 4]]).any()
+
+
+@pytest.mark.parametrize("m,k", [(1, 16), (5, 128), (33, 776), (16, 768), (2, 4096)])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_quant_silu_mul(q, dev, m, k, kind):
+    # h in fp32: exp (up to 2 steps of 2^-23 relative), 1 + e, the quotient and the product are off by at most
+    # 6 * 2^-23 together; the scale adds one rounding, the code half a step of e4m3 (2^-4 of the value, at the
+    # smallest exponent 2^-10 of the unit), over which the quotient's error may carry it
+    g = rng(2, m, k)
+    x = (g.standard_normal((m, 2 * k)) * 4).astype(np.float32)
+    x[0, 0], x[0, 1] = 80.0, -80.0
+    t = torch.from_numpy(x) if kind == "f32" else bf16_round(x)
+    xq, xs = q.qmm_fp8_quant_silu_mul(t.to(dev))
+    h = o.silu_mul(t.float().numpy())
+    s, rel = host(xs).astype(np.float64), 8 * 2.0 ** -23
+    pad = np.pad(np.abs(h), ((0, 0), (0, o.blocks(k) * 128 - k))).reshape(m, -1, 128).max(2).T
+    assert (np.abs(s - np.maximum(pad / 448, 2.0 ** -126)) <= rel * np.maximum(pad / 448, 2.0 ** -126)).all()
+    row_scale = np.repeat(s.T, 128, axis=1)[:, :k]
+    got = o.decode(host(xq.view(torch.uint8))) * row_scale
+    check(got, h, np.abs(h) * (2.0 ** -4 + 2 * rel) + row_scale * 2.0 ** -10 * (1 + 2 * rel) + 1e-37)
+
+
+# ------------------------------------------------------------------ dense
+
+SHAPES = [(1, 1, 16), (1, 16, 128), (2, 17, 144), (4, 130, 256), (16, 100, 2064), (1, 513, 8192), (3, 64, 9 * 128 + 48),
+          (17, 128, 256), (31, 129, 400), (33, 257, 1024), (64, 96, 128), (77, 1000, 2064), (128, 130, 4096),
+          (129, 256, 640), (300, 515, 1296), (512, 640, 2048)]
+
+
+def dense_case(seed, m, n, k):
+    g = rng(3, seed, m, n, k)
+    return codes8(g, n, k), scales(g, o.blocks(n), o.blocks(k)), codes8(g, m, k), scales(g, o.blocks(k), m)
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("m,n,k", SHAPES)
+def test_dense(q, dev, m, n, k, out):
+    w, ws, x, xs = dense_case(0, m, n, k)
+    y, buf = guarded((m, n), out, dev)
+    q.qmm_fp8(up(w, dev), up(ws, dev), up(x, dev), up(xs, dev), n, k, y=y)
+    torch.cuda.synchronize()
+    assert guards_intact(buf)
+    exact, mag = o.product(o.rows_f64(x, xs), o.weights_f64(w, ws))
+    check(host(y.double()), exact, bound(mag, k, out, exact))
+
+
+def test_dense_large_tiles(q, dev):
+    # enough 256 x 256 tiles for the largest shape; rows and columns end inside the last ones
+    m, n, k = 4000, 4211, 400
+    w, ws, x, xs = dense_case(1, m, n, k)
+    y, buf = guarded((m, n), torch.float32, dev)
+    q.qmm_fp8(up(w, dev), up(ws, dev), up(x, dev), up(xs, dev), n, k, y=y)
+    torch.cuda.synchronize()
+    assert guards_intact(buf)
+    pick = rng(4).choice(m, 150, replace=False)
+    exact, mag = o.product(o.rows_f64(x[pick], xs[:, pick]), o.weights_f64(w, ws))
+    check(host(y)[pick].astype(np.float64), exact, bound(mag, k, torch.float32, exact))
+    again = q.qmm_fp8(up(w, dev), up(ws, dev), up(x, dev), up(xs, dev), n, k)
+    assert torch.equal(again.view(torch.int32), y.view(torch.int32))
+
+
+@pytest.mark.parametrize("n,k", [(130, 256), (100, 2064), (48, 8192)])
+def test_dense_rows_have_the_same_bits_in_any_company(q, dev, n, k):
+    w, ws, x, xs = dense_case(2, 16, n, k)
+    wd, wsd = up(w, dev), up(ws, dev)
+    full = host(q.qmm_fp8(wd, wsd, up(x, dev), up(xs, dev), n, k))
+    for m in range(1, 16):
+        part = host(q.qmm_fp8(wd, wsd, up(x[:m], dev), up(xs[:, :m], dev), n, k))
+        assert np.array_equal(part.view(np.uint32), full[:m].view(np.uint32)), m
+
+
+@pytest.mark.parametrize("m", [2, 40, 200])
+def test_dense_values_that_are_not_finite_stay_in_their_row_and_column(q, dev, m):
+    n, k = 150, 400
+    w, ws, x, xs = dense_case(3, m, n, k)
+    clean = host(q.qmm_fp8(up(w, dev), up(ws, dev), up(x, dev), up(xs, dev), n, k))
+    x[1, 399], w[149, 3] = 0x7F, 0xFF
+    y = host(q.qmm_fp8(up(w, dev), up(ws, dev), up(x, dev), up(xs, dev), n, k))
+    assert np.isnan(y[1]).all() and np.isnan(y[:, 149]).all()
+    keep = np.ones((m, n), bool)
+    keep[1], keep[:, 149] = False, False
+    assert np.array_equal(y[keep], clean[keep])
+
+
+# ------------------------------------------------------------------ grouped
+
+def grouped_case(seed, kind, counts, n, k, x_rows, gather, lead=0, spare=0):
+    g = rng(5, seed, n, k, x_rows)
+    e, rows = len(counts), lead + sum(counts) + spare
+    off = (np.concatenate([[0], np.cumsum(counts)]) + lead).astype(np.int32)
+    index = g.integers(0, x_rows, rows).astype(np.int32) if gather else None
+    x_rows = x_rows if gather else rows
+    if kind == "fp8":
+        w, ws, x, xs = codes8(g, e, n, k), scales(g, e, o.blocks(n), o.blocks(k)), codes8(g, x_rows, k), scales(
+            g, o.blocks(k), x_rows)
+        return off, index, (w, ws, x, xs), [o.weights_f64(w[i], ws[i]) for i in range(e)], o.rows_f64(x, xs)
+    w, x = bf16_round(g.standard_normal((e, n, k))), bf16_round(g.standard_normal((x_rows, k)))
+    return off, index, (w, x), list(w.double().numpy()), x.double().numpy()
+
+
+def run_grouped(q, dev, kind, off, index, data, n, k, y):
+    idx = None if index is None else up(index, dev)
+    if kind == "fp8":
+        w, ws, x, xs = (up(a, dev) for a in data)
+        return q.qmm_fp8_grouped(w, ws, x, xs, up(off, dev), n, k, row_index=idx, y=y)
+    return q.qmm_bf16_grouped(data[0].to(dev), data[1].to(dev), up(off, dev), n, k, row_index=idx, y=y)
+
+
+GROUPS = [
+    ([1], 16, 128, 1, False, 0, 0), ([0, 0, 3, 0], 17, 144, 2, True, 0, 0), ([1, 0, 2, 1, 0, 1], 130, 1040, 4, True, 0, 3),
+    ([5, 0, 40, 0, 0, 1, 2], 100, 400, 30, True, 2, 1), ([20, 33, 0, 31], 129, 256, 50, False, 0, 5),
+    ([64, 1, 65, 90], 257, 272, 70, True, 0, 0), ([300, 0, 129], 140, 384, 200, True, 1, 7), ([0, 0], 40, 128, 3, True, 2, 2),
+    ([3] * 70 + [0] * 60 + [1], 24, 128, 9, True, 0, 0), ([40] * 70, 24, 128, 9, True, 0, 0),
+]
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["fp8", "bf16"])
+@pytest.mark.parametrize("counts,n,k,x_rows,gather,lead,spare", GROUPS)
+def test_grouped(q, dev, kind, out, counts, n, k, x_rows, gather, lead, spare):
+    off, index, data, w, x = grouped_case(0, kind, counts, n, k, x_rows, gather, lead, spare)
+    rows = lead + sum(counts) + spare
+    y, buf = guarded((rows, n), out, dev)
+    y.fill_(-7.0)
+    run_grouped(q, dev, kind, off, index, data, n, k, y)
+    torch.cuda.synchronize()
+    assert guards_intact(buf)
+    exact, mag = o.grouped(x, w, off, np.full((rows, n), -7.0), index)
+    check(host(y.double()), exact, bound(mag, k, out, exact, kind == "bf16"))
+    outside = np.ones(rows, bool)
+    outside[off[0]:off[-1]] = False
+    assert (host(y.float())[outside] == -7.0).all()
+
+
+@pytest.mark.parametrize("kind", ["fp8", "bf16"])
+@pytest.mark.parametrize("counts", [[2, 0, 3], [40, 0, 60]])
+def test_grouped_indices_outside_x_give_zeros(q, dev, kind, counts):
+    n, k = 50, 256
+    off, index, data, w, x = grouped_case(1, kind, counts, n, k, 6, True)
+    index[1], index[3], index[4] = -1, 6, 2 ** 31 - 1
+    y = torch.full((len(index), n), 5.0, device=dev)
+    run_grouped(q, dev, kind, off, index, data, n, k, y)
+    exact, mag = o.grouped(x, w, off, np.zeros((len(index), n)), index)
+    got = host(y.double())
+    assert (got[[1, 3, 4]] == 0).all()
+    check(got, exact, bound(mag, k, torch.float32, exact, kind == "bf16"))
+    # x without any row: zeros everywhere
+    empty = tuple(a[:, :0] if a.ndim == 2 and kind == "fp8" and i == 3 else a[:0] if i == len(data) - 1 or i == 2 else a
+                  for i, a in enumerate(data))
+    y.fill_(5.0)
+    run_grouped(q, dev, kind, off, index, empty, n, k, y)
+    assert (host(y) == 0).all()
+
+
+@pytest.mark.parametrize("kind", ["fp8", "bf16"])
+def test_grouped_offsets_beyond_y_are_clamped(q, dev, kind):
+    counts, n, k = [20, 30, 14], 40, 128
+    off, index, data, w, x = grouped_case(2, kind, counts, n, k, 64, False)
+    y, buf = guarded((64, n), torch.float32, dev)
+    wide = off.copy()
+    wide[0], wide[-1] = -5, 1000
+    run_grouped(q, dev, kind, wide, index, data, n, k, y)
+    torch.cuda.synchronize()
+    assert guards_intact(buf)
+    exact, mag = o.grouped(x, w, off, np.zeros((64, n)), index)
+    check(host(y.double()), exact, bound(mag, k, torch.float32, exact, kind == "bf16"))
+
+
+@pytest.mark.parametrize("kind", ["fp8", "bf16"])
+def test_grouped_no_rows_and_fresh_output(q, dev, kind):
+    off, index, data, _, _ = grouped_case(3, kind, [0, 0, 0], 24, 128, 4, True)
+    y = run_grouped(q, dev, kind, off, index, data, 24, 128, None)
+    assert y.shape == (0, 24)
+    off, index, data, _, _ = grouped_case(3, kind, [2, 0, 1], 24, 128, 4, True, spare=2)
+    y = host(run_grouped(q, dev, kind, off, index, data, 24, 128, None))
+    assert (y[3:] == 0).all() and (y[:3] != 0).any()
