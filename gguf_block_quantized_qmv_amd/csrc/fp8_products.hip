@@ -22,6 +22,8 @@
 // of its value) is a hundred times the native sums' error, are kNative where
 // the matrix cores bound the product and kExact where the weight stream does.
 // bf16 operands (kBf16) take two v_mfma_f32_16x16x32_bf16 a block.
+#include <type_traits>
+
 #include "fp8_internal.h"
 #include "fp8_layout.h"
 #include "qmv_device.h"
@@ -79,25 +81,28 @@ struct Operand<kBf16> {
   }
 };
 
-// acc += scale * (A B) over one block; scale is not used by bf16.
+// d = from + A B over one block.
 template <Kind KIND>
-__device__ __forceinline__ void mma_block(const Operand<KIND> &a, const Operand<KIND> &b, const float scale, v4f &acc) {
-  if constexpr (KIND == kBf16) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[h], b.v[h], acc, 0, 0, 0);
+__device__ __forceinline__ v4f mma_block(const Operand<KIND> &a, const Operand<KIND> &b, v4f d) {
+  if constexpr (KIND == kNative) {
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, d, 0, 0, 0, 0, 0, 0);
   } else {
-    v4f d = {0.0f, 0.0f, 0.0f, 0.0f};
-    if constexpr (KIND == kNative) {
-      d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a.v, b.v, d, 0, 0, 0, 0, 0, 0);
-    } else {
+    constexpr int kParts = KIND == kExact ? 4 : 2;
 #pragma unroll
-      for (int h = 0; h < 4; ++h) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[h], b.v[h], d, 0, 0, 0);
-    }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(scale, d[e], acc[e]);
+    for (int h = 0; h < kParts; ++h) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[h], b.v[h], d, 0, 0, 0);
+    return d;
   }
 }
 
+// acc += scale * d
+__device__ __forceinline__ void scaled_add(const float scale, const v4f d, v4f &acc) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(scale, d[e], acc[e]);
+}
+
+constexpr v4f kZero4 = {0.0f, 0.0f, 0.0f, 0.0f};
+
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
 
 // Rows of expert e, clamped to y.
@@ -201,7 +206,10 @@ __global__ __launch_bounds__(NW * 64) void product_stream_kernel(const ProductAr
             Operand<KIND> a, b;
             a.set(wf[u]);
             b.set(xf[u]);
-            mma_block<KIND>(a, b, FP8 ? xs[u] * ws[u] : 0.0f, acc);
+            if constexpr (FP8)
+              scaled_add(xs[u] * ws[u], mma_block<KIND>(a, b, kZero4), acc);
+            else
+              acc = mma_block<KIND>(a, b, acc);
           }
           load(i0 + u + kDepth, u);
         }
@@ -277,7 +285,7 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
   constexpr bool FP8 = is_e4m3(KIND);
   __shared__ __attribute__((aligned(1024))) uint8_t stage0[S::kStageBytes];
   __shared__ __attribute__((aligned(1024))) uint8_t stage1[S::kStageBytes];
-  __shared__ float scale0[FP8 ? S::BM : 64], scale1[FP8 ? S::BM : 64];
+  __shared__ float scale0[(S::BM + 63) / 64 * 64], scale1[(S::BM + 63) / 64 * 64];
   const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int n_tiles = fp8::ceil_div(p.n, S::BN);
 
@@ -329,54 +337,79 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
     nt = in / high;
     m0 = (band * 8 + in - nt * high) * S::BM;
   }
+  // uniform, but divided on vector lanes: into scalar registers
+  m0 = uniform(m0);
+  nt = uniform(nt);
+  begin = uniform(begin);
+  end = uniform(end);
   const int n0 = nt * S::BN;
-  const int blk0 = GROUPED ? 0 : (int)((int64_t)p.nb * part / p.splits);
-  const int blk1 = GROUPED ? p.nb : (int)((int64_t)p.nb * (part + 1) / p.splits);
+  const int blk0 = GROUPED ? 0 : uniform((int)((int64_t)p.nb * part / p.splits));
+  const int blk1 = GROUPED ? p.nb : uniform((int)((int64_t)p.nb * (part + 1) / p.splits));
 
-  // this lane's direct loads: row q * 8 + lane / 8 of the stage, chunk by the slot
-  const uint8_t *from[S::kLoads];
+  // this lane's direct loads: row q * 8 + lane / 8 of the stage, chunk by the
+  // slot; a wave-uniform base and an offset of the lane (32 bits suffice within
+  // the rows of one dense tile, not for rows gathered from all of x)
+  using Offset = std::conditional_t<GROUPED, uint64_t, uint32_t>;
+  const uint8_t *xbase = p.x + (GROUPED ? 0 : (size_t)m0 * p.k_bytes);
+  const uint8_t *wbase = p.w + ((size_t)expert * p.n + n0) * p.k_bytes;
+  Offset from[S::kLoads];
   int chunk_at[S::kLoads];
+  int src[S::kLoads];
 #pragma unroll
   for (int i = 0; i < S::kLoads; ++i) {
     const int row = (wave * S::kLoads + i) * 8 + (lane >> 3);
-    chunk_at[i] = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
-    if (row < S::BM) {
-      int src;
-      source_row(p, m0 + row < end ? m0 + row : end - 1, src);
-      from[i] = p.x + (size_t)src * p.k_bytes;
+    if (wave * S::kLoads + i < S::BM / 8) {
+      const int at = m0 + row < end ? m0 + row : end - 1;
+      src[i] = GROUPED ? at : at - m0;
     } else {
-      const int wrow = n0 + row - S::BM;
-      from[i] = p.w + ((size_t)expert * p.n + (wrow < p.n ? wrow : p.n - 1)) * p.k_bytes;
+      src[i] = n0 + row - S::BM < p.n ? row - S::BM : p.n - 1 - n0;
     }
-    from[i] += chunk_at[i] + (size_t)blk0 * 128;
+    chunk_at[i] = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
   }
-  const float *scale_from = nullptr;
-  if (FP8 && wave < S::BM / 64 + (S::BM % 64 != 0)) {
-    const int row = m0 + wave * 64 + lane;
-    int src;
-    source_row(p, row < end ? row : end - 1, src);
-    scale_from = p.x_scale + src + (size_t)blk0 * p.x_rows;
-  }
-  const int tail = p.k_bytes & 127;   // bytes of a partial last block
-  auto issue = [&](int b, uint8_t *stage, float *scale) {
-    uint8_t *to = stage + wave * S::kLoads * 1024;
-    if (tail && b == p.nb - 1) {
+  if constexpr (GROUPED) {
+    if (p.index) {   // all index loads before the first use
+      int found[S::kLoads];
+#pragma unroll
+      for (int i = 0; i < S::kLoads; ++i) found[i] = p.index[wave * S::kLoads + i < S::BM / 8 ? src[i] : begin];
 #pragma unroll
       for (int i = 0; i < S::kLoads; ++i)
-        load_lds16(chunk_at[i] < tail ? from[i] : reinterpret_cast<const uint8_t *>(g_zeros), to + i * 1024);
-    } else {
+        if (wave * S::kLoads + i < S::BM / 8) src[i] = (unsigned)found[i] < (unsigned)p.x_rows ? found[i] : 0;
+    }
+  }
 #pragma unroll
-      for (int i = 0; i < S::kLoads; ++i) {
-        load_lds16(from[i], to + i * 1024);
-        from[i] += 128;
-      }
-    }
+  for (int i = 0; i < S::kLoads; ++i) from[i] = (Offset)src[i] * (Offset)p.k_bytes + (Offset)chunk_at[i];
+  // the scales of x, 64 rows a wave (waves past the tile's rows bring the same
+  // values again: no branch in the loop)
+  constexpr int kScaleRows = (S::BM + 63) / 64 * 64;
+  const int scale_to = wave * 64 % kScaleRows;
+  uint32_t scale_from = 0;
+  if constexpr (FP8) {
+    const int row = m0 + scale_to + lane;
+    int at;
+    source_row(p, row < end ? row : end - 1, at);
+    scale_from = (uint32_t)at;
+  }
+  const int tail = p.k_bytes & 127;   // bytes of a partial last block
+  // one of the wave's direct loads of block b; the lane's offset is hidden from
+  // the optimiser, which would keep a 64-bit pointer of its own per load
+  auto load_piece = [&](int i, int b, uint8_t *stage, bool last) {
+    asm("" : "+v"(from[i]));
+    const uint8_t *at = (wave * S::kLoads + i < S::BM / 8 ? xbase : wbase) + (size_t)b * 128 + from[i];
+    if (last && chunk_at[i] >= tail) at = reinterpret_cast<const uint8_t *>(g_zeros);
+    load_lds16(at, stage + (wave * S::kLoads + i) * 1024);
+  };
+  auto load_scales = [&](int b, float *scale) {
     if constexpr (FP8) {
-      if (S::BM % 64 == 0 ? wave < S::BM / 64 : wave == 0 && lane < S::BM) {
-        load_lds4(scale_from, scale + wave * 64);
-        scale_from += p.x_rows;
-      }
+      asm("" : "+v"(scale_from));
+      load_lds4(p.x_scale + (size_t)b * p.x_rows + scale_from, scale + scale_to);
     }
+  };
+  // all loads of block b, which may be the partial last one
+  auto issue = [&](int b, uint8_t *stage, float *scale) {
+    const bool partial = tail != 0 && b == p.nb - 1;
+#pragma unroll
+    for (int i = 0; i < S::kLoads; ++i) load_piece(i, b, stage, partial);
+    load_scales(b, scale);
   };
 
   const int wm = wave / S::WN, wn = wave % S::WN;
@@ -386,7 +419,10 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
   const int w_at = (S::BM + wn * S::TN * 16) * kStageRow + frag_at;
   const int col0 = n0 + wn * S::TN * 16;
   const int sblk = (col0 < p.n ? col0 : p.n - 1) >> 7;
-  const float *wsp = FP8 ? p.w_scale + ((size_t)expert * fp8::ceil_div(p.n, 128) + sblk) * p.nb : nullptr;
+  // the scale of this wave's columns, read a block ahead (a vector load: a scalar
+  // one would make every wait for an LDS read of its block a full one)
+  const float *wsp = FP8 ? p.w_scale + ((size_t)expert * fp8::ceil_div(p.n, 128) + uniform(sblk)) * p.nb : nullptr;
+  auto scale_of = [&](int b) { return FP8 ? wsp[b < p.nb ? b : p.nb - 1] : 0.0f; };
 
   v4f acc[S::TM][S::TN];
 #pragma unroll
@@ -394,38 +430,88 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
 #pragma unroll
     for (int j = 0; j < S::TN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
-  auto compute = [&](int b, const uint8_t *stage, const float *scale) {
-    const float ws = FP8 ? wsp[b] : 0.0f;
-    Operand<KIND> wf[S::TN];
-#pragma unroll
-    for (int j = 0; j < S::TN; ++j) {
+  // One block: the wave's weight operands stay, the rows of x pass one 16-row
+  // tile after the other. A tile's products are added one tile later, so that
+  // the fma of one run beside the matrix instructions of the next. With
+  // next_too the loads of the next block (a whole one) go out over the first half.
+  auto compute = [&](auto next_too, int b, float ws, const uint8_t *stage, const float *scale, uint8_t *next, float *next_scale) {
+    constexpr int kEvery = (S::kLoads + (S::TM + 1) / 2 - 1) / ((S::TM + 1) / 2);
+    auto read = [&](int lo, int hi, int rows16, Operand<KIND> &to) {
       Frag f;
-      f.lo = *reinterpret_cast<const v4i *>(stage + w_at + j * 2048);
-      f.hi = *reinterpret_cast<const v4i *>(stage + (w_at ^ 64) + j * 2048);
-      wf[j].set(f);
-    }
+      f.lo = *reinterpret_cast<const v4i *>(stage + lo + rows16 * 2048);
+      f.hi = *reinterpret_cast<const v4i *>(stage + hi + rows16 * 2048);
+      to.set(f);
+    };
+    Operand<KIND> wf[S::TN], xf[2];
+    float s[2];
+    v4f d[2][S::TN];
+    if constexpr (FP8) s[0] = scale[wm * S::TM * 16 + r];
+    read(x_at, x_at ^ 64, 0, xf[0]);
+#pragma unroll
+    for (int j = 0; j < S::TN; ++j) read(w_at, w_at ^ 64, j, wf[j]);
 #pragma unroll
     for (int i = 0; i < S::TM; ++i) {
-      Frag f;
-      f.lo = *reinterpret_cast<const v4i *>(stage + x_at + i * 2048);
-      f.hi = *reinterpret_cast<const v4i *>(stage + (x_at ^ 64) + i * 2048);
-      Operand<KIND> xf;
-      xf.set(f);
-      const float s = FP8 ? scale[(wm * S::TM + i) * 16 + r] * ws : 0.0f;
+      const float before = i > 0 ? s[(i - 1) & 1] * ws : 0.0f;
+      if (i + 1 < S::TM) {
+        if constexpr (FP8) s[(i + 1) & 1] = scale[(wm * S::TM + i + 1) * 16 + r];
+        read(x_at, x_at ^ 64, i + 1, xf[(i + 1) & 1]);
+      }
+      if constexpr (decltype(next_too)::value) {
+        if (i == 0) load_scales(b + 1, next_scale);
 #pragma unroll
-      for (int j = 0; j < S::TN; ++j) mma_block<KIND>(wf[j], xf, s, acc[i][j]);
+        for (int l = i * kEvery; l < (i + 1) * kEvery && l < S::kLoads; ++l) load_piece(l, b + 1, next, false);
+      }
+      if constexpr (FP8) {
+#pragma unroll
+        for (int j = 0; j < S::TN; ++j) {
+          d[i & 1][j] = mma_block<KIND>(wf[j], xf[i & 1], kZero4);
+          if (i > 0) scaled_add(before, d[(i - 1) & 1][j], acc[i > 0 ? i - 1 : 0][j]);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < S::TN; ++j) acc[i][j] = mma_block<KIND>(wf[j], xf[i & 1], acc[i][j]);
+      }
+      if constexpr (KIND == kNative) {
+        // the order of issue: reads of the next tile, then four fma behind each matrix instruction
+        __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
+#pragma unroll
+        for (int j = 0; j < S::TN; ++j) {
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (FP8) {
+#pragma unroll
+      for (int j = 0; j < S::TN; ++j) scaled_add(s[(S::TM - 1) & 1] * ws, d[(S::TM - 1) & 1][j], acc[S::TM - 1][j]);
     }
   };
 
   issue(blk0, stage0, scale0);
-  for (int b = blk0; b < blk1; b += 2) {
+  int b = blk0;
+  float ws = scale_of(b);
+  for (; b + 3 < blk1; b += 2) {   // the loads sent here are all of whole blocks
     stage_barrier();
-    if (b + 1 < blk1) issue(b + 1, stage1, scale1);
-    compute(b, stage0, scale0);
-    if (b + 1 >= blk1) break;
+    const float ws1 = scale_of(b + 1);
+    compute(std::true_type{}, b, ws, stage0, scale0, stage1, scale1);
     stage_barrier();
-    if (b + 2 < blk1) issue(b + 2, stage0, scale0);
-    compute(b + 1, stage1, scale1);
+    ws = scale_of(b + 2);
+    compute(std::true_type{}, b + 1, ws1, stage1, scale1, stage0, scale0);
+  }
+  const int left = blk1 - b;       // one to three blocks, the first of them on its way
+  const float ws1 = scale_of(b + 1), ws2 = scale_of(b + 2);
+  stage_barrier();
+  if (left > 1) issue(b + 1, stage1, scale1);
+  compute(std::false_type{}, b, ws, stage0, scale0, nullptr, nullptr);
+  if (left > 1) {
+    stage_barrier();
+    if (left > 2) issue(b + 2, stage0, scale0);
+    compute(std::false_type{}, b + 1, ws1, stage1, scale1, nullptr, nullptr);
+    if (left > 2) {
+      stage_barrier();
+      compute(std::false_type{}, b + 2, ws2, stage0, scale0, nullptr, nullptr);
+    }
   }
 
   // lane: columns 4 g .. 4 g + 3 of row r of each 16 x 16 tile
