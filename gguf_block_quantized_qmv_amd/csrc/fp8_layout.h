@@ -33,8 +33,32 @@ struct DensePlan {
   int splits;    // parts of k, summed by a second launch when more than one
 };
 
-// Waves of a streaming workgroup: each takes every waves-th block of 128.
-constexpr int stream_waves(int nb) { return nb >= 64 ? 16 : nb >= 16 ? 8 : 4; }
+// The weight-streaming kernel: `tile` weight rows (a multiple of four, so that
+// a lane's four results lie under one scale) and `waves` waves a workgroup.
+// The tile is the one of 16, 12 and 8 rows that spreads the workgroups most
+// evenly over the CUs; with few rows, shorter tiles keep every CU at work.
+// About sixteen waves a CU keep the memory busy.
+struct StreamPlan {
+  int tile, waves;
+};
+
+inline StreamPlan stream_plan(int n, int nb, int slots) {
+  int tile = 4;
+  int64_t best_num = 0, best_den = 1, per_cu = 1;
+  for (int t = 16; t >= 8; t -= 4) {
+    const int64_t groups = (int64_t)ceil_div(n, t) * slots, rounds = (groups + kSlots - 1) / kSlots;
+    if (groups * best_den > best_num * rounds * kSlots) {   // share of the CUs' rounds that has work
+      best_num = groups;
+      best_den = rounds * kSlots;
+      per_cu = rounds;
+      tile = t;
+    }
+  }
+  if (best_num * 2 <= kSlots) tile = 4;   // fewer than half the CUs even with tiles of 8
+  int waves = per_cu <= 1 ? 16 : per_cu <= 2 ? 8 : 4;
+  while (waves > 4 && waves > nb) waves >>= 1;
+  return StreamPlan{tile, waves};
+}
 
 inline DensePlan dense_plan(int m, int n, int k, bool y_bf16) {
   DensePlan p{m <= QMM_SAME_ROWS, kTile128, 1};

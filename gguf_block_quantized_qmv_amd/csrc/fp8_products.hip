@@ -102,6 +102,8 @@ __device__ __forceinline__ void scaled_add(const float scale, const v4f d, v4f &
 
 constexpr v4f kZero4 = {0.0f, 0.0f, 0.0f, 0.0f};
 
+__device__ const uint4 g_zeros[8] = {};   // what loads past the end of a row read: one block
+
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
 
@@ -130,22 +132,26 @@ __device__ __forceinline__ void store_y(const ProductArgs &p, int row, int col, 
 
 // ---- a few rows: stream the weights ---------------------------------------------
 //
-// A workgroup owns 16 rows of one weight matrix and up to 16 rows of x at a
-// time; wave v takes blocks v, v + NW, ... of k straight from memory into
-// MFMA fragments (no LDS), kDepth blocks in flight, and the waves' sums are
-// added in wave order. Bound by the weight stream. The order of the sums goes
-// by (n, k) alone and the columns of an MFMA do not mix, so a row of x has the
-// same bits in any company. Grouped: workgroup (t, s) serves the s-th expert
-// that has rows, and takes 16 of its rows at a time.
-constexpr int kDepth = 4;
+// A workgroup owns `tile` <= 16 rows of one weight matrix and up to 16 rows of
+// x at a time; wave v takes blocks v, v + NW, ... of k straight from memory
+// into MFMA fragments (no LDS), kDepth blocks in flight, and the waves' sums
+// are added in wave order. Bound by the weight stream. The host chooses the
+// tile so that every CU gets the same number of workgroups (a tile shorter
+// than 16 rows repeats its last row: matrix work, no memory traffic). The order
+// of the sums goes by (n, k) alone and the columns of an MFMA do not mix, so a
+// row of x has the same bits in any company. Grouped: workgroup (t, s) serves
+// the s-th expert that has rows, and takes 16 of its rows at a time.
+constexpr int kDepth = 3;
 
 template <Kind KIND, bool GROUPED, int NW>
-__global__ __launch_bounds__(NW * 64) void product_stream_kernel(const ProductArgs p) {
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) void product_stream_kernel(
+    const ProductArgs p, const int tile) {
   constexpr bool FP8 = is_e4m3(KIND);
   __shared__ float red[NW][256];
-  const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int lane = (int)threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int n0 = (int)blockIdx.x * 16;
+  const int n0 = (int)blockIdx.x * tile;
+  const int n1 = n0 + tile < p.n ? n0 + tile : p.n;
   int expert = 0, begin = 0, end = p.rows;
   if constexpr (GROUPED) {
     int want = (int)blockIdx.y, found = -1;
@@ -161,58 +167,83 @@ __global__ __launch_bounds__(NW * 64) void product_stream_kernel(const ProductAr
       want -= have;
     }
     if (found < 0) return;
-    expert = __builtin_amdgcn_readfirstlane(found);
+    expert = uniform(found);
     expert_rows(p.offsets, expert, p.rows, begin, end);
   }
-  const int wrow = n0 + r < p.n ? n0 + r : p.n - 1;
-  const uint8_t *wp = p.w + ((size_t)expert * p.n + wrow) * p.k_bytes;
-  const float *wsp = FP8 ? p.w_scale + ((size_t)expert * fp8::ceil_div(p.n, 128) + (n0 >> 7)) * p.nb : nullptr;
-  const int count = (p.nb - wave + NW - 1) / NW;   // this wave's blocks
+  // Lane offsets from scalar addresses. They are hidden from the optimiser at
+  // every use, which would otherwise keep one 64-bit address per block alive.
+  const uint8_t *wbase = p.w + ((size_t)expert * p.n + n0) * p.k_bytes;
+  uint32_t wlane = (uint32_t)(n0 + r < n1 ? r : n1 - 1 - n0) * (uint32_t)p.k_bytes + g * 16;
+  // tiles are multiples of four rows: a lane's four results share a scale
+  const float *wsbase = FP8 ? p.w_scale + (size_t)expert * fp8::ceil_div(p.n, 128) * p.nb : nullptr;
+  const int srow = n0 + g * 4 < p.n ? n0 + g * 4 : p.n - 1;
+  uint32_t wslane = FP8 ? (uint32_t)(srow >> 7) * (uint32_t)p.nb : 0;
+  const int whole = p.k_bytes >> 7, tail = p.k_bytes & 127;
 
   for (int t0 = begin; t0 < end; t0 += 16) {
     int src;
     source_row(p, t0 + r < end ? t0 + r : end - 1, src);
-    const uint8_t *xp = p.x + (size_t)src * p.k_bytes;
-    const float *xsp = FP8 ? p.x_scale + src : nullptr;
+    using Offset = std::conditional_t<GROUPED, uint64_t, uint32_t>;   // dense: within 16 rows
+    Offset xlane = (Offset)src * (Offset)p.k_bytes + (Offset)(g * 16);
+    uint32_t xslane = (uint32_t)src;
 
     Frag wf[kDepth], xf[kDepth];
     float xs[kDepth], ws[kDepth];
-    auto load = [&](int i, int u) {
-      const int b = wave + NW * (i < count ? i : count - 1);
-      const int at = b * 128 + g * 16;
-      const bool lo = at < p.k_bytes, hi = at + 64 < p.k_bytes;   // chunks past the row read as zeros
-      const v4i zero = {0, 0, 0, 0};
-      const v4i a = *reinterpret_cast<const v4i *>(wp + (lo ? at : 0));
-      const v4i c = *reinterpret_cast<const v4i *>(wp + (hi ? at + 64 : 0));
-      const v4i d = *reinterpret_cast<const v4i *>(xp + (lo ? at : 0));
-      const v4i e = *reinterpret_cast<const v4i *>(xp + (hi ? at + 64 : 0));
-      wf[u].lo = lo ? a : zero;
-      wf[u].hi = hi ? c : zero;
-      xf[u].lo = lo ? d : zero;
-      xf[u].hi = hi ? e : zero;
+    // Block b (past the last whole one: zeros, so that every pass of the loop
+    // sends the same loads and each wait counts exactly those behind it).
+    auto load_scales = [&](int b, int u, bool ok) {
       if constexpr (FP8) {
-        xs[u] = xsp[(size_t)b * p.x_rows];
-        ws[u] = wsp[b];
+        asm("" : "+v"(xslane), "+v"(wslane));
+        const float *zeros = reinterpret_cast<const float *>(g_zeros);
+        xs[u] = (ok ? p.x_scale + (size_t)b * p.x_rows : zeros)[ok ? xslane : 0];
+        ws[u] = (ok ? wsbase + b : zeros)[ok ? wslane : 0];
       }
     };
-    v4f acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (count > 0) {
+    auto load = [&](int b, int u) {
+      asm("" : "+v"(wlane), "+v"(xlane));
+      const bool ok = b < whole;
+      const uint8_t *zeros = reinterpret_cast<const uint8_t *>(g_zeros);
+      const uint8_t *w = (ok ? wbase + (size_t)b * 128 : zeros) + (ok ? wlane : 0);
+      const uint8_t *x = (ok ? p.x + (size_t)b * 128 : zeros) + (ok ? xlane : 0);
+      wf[u].lo = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(w));
+      wf[u].hi = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(w + 64));
+      xf[u].lo = *reinterpret_cast<const v4i *>(x);
+      xf[u].hi = *reinterpret_cast<const v4i *>(x + 64);
+      load_scales(b, u, ok);
+    };
+    v4f acc = kZero4;
+    auto use = [&](int u) {
+      Operand<KIND> a, c;
+      a.set(wf[u]);
+      c.set(xf[u]);
+      if constexpr (FP8)
+        scaled_add(xs[u] * ws[u], mma_block<KIND>(a, c, kZero4), acc);
+      else
+        acc = mma_block<KIND>(a, c, acc);
+    };
 #pragma unroll
-      for (int u = 0; u < kDepth; ++u) load(u, u);
-      for (int i0 = 0; i0 < count; i0 += kDepth)
+    for (int u = 0; u < kDepth; ++u) load(wave + u * NW, u);
+    for (int b = wave; b < whole; b += kDepth * NW)
 #pragma unroll
-        for (int u = 0; u < kDepth; ++u) {
-          if (i0 + u < count) {
-            Operand<KIND> a, b;
-            a.set(wf[u]);
-            b.set(xf[u]);
-            if constexpr (FP8)
-              scaled_add(xs[u] * ws[u], mma_block<KIND>(a, b, kZero4), acc);
-            else
-              acc = mma_block<KIND>(a, b, acc);
-          }
-          load(i0 + u + kDepth, u);
-        }
+      for (int u = 0; u < kDepth; ++u) {
+        use(u);
+        load(b + (u + kDepth) * NW, u);
+        __builtin_amdgcn_sched_barrier(0);   // one block's widened operands at a time
+      }
+    if (tail && wave == whole % NW) {   // the partial last block: zeros past the row
+      const v4i none = {0, 0, 0, 0};
+      wf[0].lo = wf[0].hi = xf[0].lo = xf[0].hi = none;
+      const uint8_t *w = wbase + (size_t)whole * 128 + wlane, *x = p.x + (size_t)whole * 128 + xlane;
+      if (g * 16 < tail) {
+        wf[0].lo = *reinterpret_cast<const v4i *>(w);
+        xf[0].lo = *reinterpret_cast<const v4i *>(x);
+      }
+      if (g * 16 + 64 < tail) {
+        wf[0].hi = *reinterpret_cast<const v4i *>(w + 64);
+        xf[0].hi = *reinterpret_cast<const v4i *>(x + 64);
+      }
+      load_scales(whole, 0, true);
+      use(0);
     }
     // lane l holds columns 4 g .. 4 g + 3 of row r of x
     *reinterpret_cast<v4f *>(&red[wave][r * 16 + g * 4]) = acc;
@@ -222,7 +253,7 @@ __global__ __launch_bounds__(NW * 64) void product_stream_kernel(const ProductAr
       float sum = red[0][threadIdx.x];
 #pragma unroll
       for (int v = 1; v < NW; ++v) sum += red[v][threadIdx.x];
-      if (row < end && col < p.n) {
+      if (row < end && col < n1) {
         int at;
         store_y(p, row, col, source_row(p, row, at) ? sum : 0.0f);
       }
@@ -241,8 +272,6 @@ __global__ __launch_bounds__(NW * 64) void product_stream_kernel(const ProductAr
 // chunk) free of bank conflicts. The direct loads write LDS in lane order, so
 // the permutation is applied to the global address each lane reads.
 constexpr int kStageRow = 128;
-
-__device__ const uint4 g_zeros[1] = {};
 
 template <int BM_, int BN_, int WM_, int WN_>
 struct Shape {
@@ -597,11 +626,13 @@ int launch_tiles(int tile, const ProductArgs &a, hipStream_t s) {
 
 template <Kind KIND, bool GROUPED>
 int launch_stream(const ProductArgs &a, hipStream_t s) {
-  const dim3 grid((unsigned)fp8::ceil_div(a.n, 16), GROUPED ? (unsigned)(a.rows < a.n_experts ? a.rows : a.n_experts) : 1u);
-  switch (fp8::stream_waves(a.nb)) {
-    case 16: return launch_kernel("product_stream_kernel", product_stream_kernel<KIND, GROUPED, 16>, grid, dim3(1024), 0, s, a);
-    case 8: return launch_kernel("product_stream_kernel", product_stream_kernel<KIND, GROUPED, 8>, grid, dim3(512), 0, s, a);
-    default: return launch_kernel("product_stream_kernel", product_stream_kernel<KIND, GROUPED, 4>, grid, dim3(256), 0, s, a);
+  const int slots = GROUPED ? (a.rows < a.n_experts ? a.rows : a.n_experts) : 1;
+  const fp8::StreamPlan plan = fp8::stream_plan(a.n, a.nb, slots);
+  const dim3 grid((unsigned)fp8::ceil_div(a.n, plan.tile), (unsigned)slots);
+  switch (plan.waves) {
+    case 16: return launch_kernel("product_stream_kernel", product_stream_kernel<KIND, GROUPED, 16>, grid, dim3(1024), 0, s, a, plan.tile);
+    case 8: return launch_kernel("product_stream_kernel", product_stream_kernel<KIND, GROUPED, 8>, grid, dim3(512), 0, s, a, plan.tile);
+    default: return launch_kernel("product_stream_kernel", product_stream_kernel<KIND, GROUPED, 4>, grid, dim3(256), 0, s, a, plan.tile);
   }
 }
 
