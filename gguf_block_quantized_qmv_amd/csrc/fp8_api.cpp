@@ -60,6 +60,8 @@ int grouped(const void *w, size_t w_bytes, const float *w_scale, const void *x, 
   if (w_bytes != wb) return QMV_ERR_SIZE;
   if (rows == 0) return QMV_OK;
   if (!qmv::fp8::grouped_fits_grid(rows, n, n_experts)) return QMV_ERR_RANGE;
+  // rows are gathered by 32-bit byte offsets
+  if (row_index && (size_t)x_rows * k * value_bytes > UINT32_MAX) return QMV_ERR_RANGE;
   // with no row of x every index is out of range, and x itself may be null
   if (!y || (x_rows > 0 && (!x || (e4m3 && !x_scale)))) return QMV_ERR_NULL;
   if (!aligned(w, 16) || !aligned(x, 16) || !aligned(y, 16) || !aligned(w_scale, 4) || !aligned(x_scale, 4) ||

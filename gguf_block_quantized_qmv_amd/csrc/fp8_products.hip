@@ -284,13 +284,21 @@ struct Shape {
   static_assert(BN / WN <= 128 && 128 % (BN / WN) == 0, "a wave's columns lie under one weight scale");
 };
 
-__device__ __forceinline__ void load_lds16(const uint8_t *g, uint8_t *l) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)g,
-                                   (__attribute__((address_space(3))) void *)l, 16, 0, 0);
+// Buffer form of the direct load: LDS at `to` + 16 (or 4) bytes a lane gets
+// the bytes at base + at + step; at or beyond `size` it gets zeros. (Unlike the
+// global form it does not make the compiler drain the LDS reads in flight.)
+typedef __amdgpu_buffer_rsrc_t Buffer;
+__device__ __forceinline__ Buffer buffer_of(const void *base, uint32_t size) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, (int)size, 0x00020000);
 }
-__device__ __forceinline__ void load_lds4(const float *g, float *l) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)g,
-                                   (__attribute__((address_space(3))) void *)l, 4, 0, 0);
+constexpr uint32_t kOutside = 0xFFFFFFFFu;   // an offset past every buffer
+__device__ __forceinline__ void load_lds16(Buffer from, uint32_t at, uint32_t step, void *to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void *)to, 16, (int)at, (int)step,
+                                           0, 0);
+}
+__device__ __forceinline__ void load_lds4(Buffer from, uint32_t at, uint32_t step, void *to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void *)to, 4, (int)at, (int)step,
+                                           0, 0);
 }
 
 // Every direct load of this wave has landed and every LDS read has returned,
@@ -375,38 +383,37 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
   const int blk0 = GROUPED ? 0 : uniform((int)((int64_t)p.nb * part / p.splits));
   const int blk1 = GROUPED ? p.nb : uniform((int)((int64_t)p.nb * (part + 1) / p.splits));
 
-  // this lane's direct loads: row q * 8 + lane / 8 of the stage, chunk by the
-  // slot; a wave-uniform base and an offset of the lane (32 bits suffice within
-  // the rows of one dense tile, not for rows gathered from all of x)
-  using Offset = std::conditional_t<GROUPED, uint64_t, uint32_t>;
-  const uint8_t *xbase = p.x + (GROUPED ? 0 : (size_t)m0 * p.k_bytes);
-  const uint8_t *wbase = p.w + ((size_t)expert * p.n + n0) * p.k_bytes;
-  Offset from[S::kLoads];
+  // This lane's direct loads: row q * 8 + lane / 8 of the stage, chunk by the
+  // slot, as an offset from a scalar base: the tile's first row of w, and of x
+  // unless its rows are gathered (from all of x, which the host then keeps under
+  // 4 GiB).
+  const bool gather = GROUPED && p.index;
+  const Buffer wbuf = buffer_of(p.w + ((size_t)expert * p.n + n0) * p.k_bytes,
+                                (uint32_t)(p.n - n0 < S::BN ? p.n - n0 : S::BN) * (uint32_t)p.k_bytes);
+  const int x_first = gather ? 0 : m0, x_count = gather ? p.x_rows : end - m0 < S::BM ? end - m0 : S::BM;
+  const Buffer xbuf = buffer_of(p.x + (size_t)x_first * p.k_bytes, (uint32_t)x_count * (uint32_t)p.k_bytes);
+  uint32_t from[S::kLoads];
   int chunk_at[S::kLoads];
   int src[S::kLoads];
 #pragma unroll
   for (int i = 0; i < S::kLoads; ++i) {
     const int row = (wave * S::kLoads + i) * 8 + (lane >> 3);
-    if (wave * S::kLoads + i < S::BM / 8) {
-      const int at = m0 + row < end ? m0 + row : end - 1;
-      src[i] = GROUPED ? at : at - m0;
-    } else {
-      src[i] = n0 + row - S::BM < p.n ? row - S::BM : p.n - 1 - n0;
-    }
     chunk_at[i] = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
+    if (wave * S::kLoads + i < S::BM / 8)
+      src[i] = (m0 + row < end ? m0 + row : end - 1) - x_first;
+    else
+      src[i] = n0 + row - S::BM < p.n ? row - S::BM : p.n - 1 - n0;
   }
-  if constexpr (GROUPED) {
-    if (p.index) {   // all index loads before the first use
-      int found[S::kLoads];
+  if (gather) {   // all index loads before the first use
+    int found[S::kLoads];
 #pragma unroll
-      for (int i = 0; i < S::kLoads; ++i) found[i] = p.index[wave * S::kLoads + i < S::BM / 8 ? src[i] : begin];
+    for (int i = 0; i < S::kLoads; ++i) found[i] = p.index[wave * S::kLoads + i < S::BM / 8 ? src[i] : m0];
 #pragma unroll
-      for (int i = 0; i < S::kLoads; ++i)
-        if (wave * S::kLoads + i < S::BM / 8) src[i] = (unsigned)found[i] < (unsigned)p.x_rows ? found[i] : 0;
-    }
+    for (int i = 0; i < S::kLoads; ++i)
+      if (wave * S::kLoads + i < S::BM / 8) src[i] = (unsigned)found[i] < (unsigned)p.x_rows ? found[i] : 0;
   }
 #pragma unroll
-  for (int i = 0; i < S::kLoads; ++i) from[i] = (Offset)src[i] * (Offset)p.k_bytes + (Offset)chunk_at[i];
+  for (int i = 0; i < S::kLoads; ++i) from[i] = (uint32_t)src[i] * (uint32_t)p.k_bytes + (uint32_t)chunk_at[i];
   // the scales of x, 64 rows a wave (waves past the tile's rows bring the same
   // values again: no branch in the loop)
   constexpr int kScaleRows = (S::BM + 63) / 64 * 64;
@@ -416,22 +423,21 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
     const int row = m0 + scale_to + lane;
     int at;
     source_row(p, row < end ? row : end - 1, at);
-    scale_from = (uint32_t)at;
+    scale_from = (uint32_t)at * 4;
   }
   const int tail = p.k_bytes & 127;   // bytes of a partial last block
-  // one of the wave's direct loads of block b; the lane's offset is hidden from
-  // the optimiser, which would keep a 64-bit pointer of its own per load
+  // one of the wave's direct loads of block b
   auto load_piece = [&](int i, int b, uint8_t *stage, bool last) {
-    asm("" : "+v"(from[i]));
-    const uint8_t *at = (wave * S::kLoads + i < S::BM / 8 ? xbase : wbase) + (size_t)b * 128 + from[i];
-    if (last && chunk_at[i] >= tail) at = reinterpret_cast<const uint8_t *>(g_zeros);
-    load_lds16(at, stage + (wave * S::kLoads + i) * 1024);
+    const uint32_t at = last && chunk_at[i] >= tail ? kOutside : from[i];
+    uint8_t *to = stage + (wave * S::kLoads + i) * 1024;
+    if (wave * S::kLoads + i < S::BM / 8)
+      load_lds16(xbuf, at, (uint32_t)b * 128, to);
+    else
+      load_lds16(wbuf, at, (uint32_t)b * 128, to);
   };
   auto load_scales = [&](int b, float *scale) {
-    if constexpr (FP8) {
-      asm("" : "+v"(scale_from));
-      load_lds4(p.x_scale + (size_t)b * p.x_rows + scale_from, scale + scale_to);
-    }
+    if constexpr (FP8)
+      load_lds4(buffer_of(p.x_scale + (size_t)b * p.x_rows, (uint32_t)p.x_rows * 4), scale_from, 0, scale + scale_to);
   };
   // all loads of block b, which may be the partial last one
   auto issue = [&](int b, uint8_t *stage, float *scale) {
@@ -464,7 +470,10 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
   // the fma of one run beside the matrix instructions of the next. With
   // next_too the loads of the next block (a whole one) go out over the first half.
   auto compute = [&](auto next_too, int b, float ws, const uint8_t *stage, const float *scale, uint8_t *next, float *next_scale) {
-    constexpr int kEvery = (S::kLoads + (S::TM + 1) / 2 - 1) / ((S::TM + 1) / 2);
+#ifndef VEVERY
+#define VEVERY ((S::kLoads + (S::TM + 1) / 2 - 1) / ((S::TM + 1) / 2))
+#endif
+    constexpr int kEvery = VEVERY;
     auto read = [&](int lo, int hi, int rows16, Operand<KIND> &to) {
       Frag f;
       f.lo = *reinterpret_cast<const v4i *>(stage + lo + rows16 * 2048);
@@ -495,19 +504,12 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
         for (int j = 0; j < S::TN; ++j) {
           d[i & 1][j] = mma_block<KIND>(wf[j], xf[i & 1], kZero4);
           if (i > 0) scaled_add(before, d[(i - 1) & 1][j], acc[i > 0 ? i - 1 : 0][j]);
+          // keeps the fma of a result TN matrix instructions behind it
+          if (KIND == kNative) __builtin_amdgcn_sched_barrier(0);
         }
       } else {
 #pragma unroll
         for (int j = 0; j < S::TN; ++j) acc[i][j] = mma_block<KIND>(wf[j], xf[i & 1], acc[i][j]);
-      }
-      if constexpr (KIND == kNative) {
-        // the order of issue: reads of the next tile, then four fma behind each matrix instruction
-        __builtin_amdgcn_sched_group_barrier(0x100, 3, 0);
-#pragma unroll
-        for (int j = 0; j < S::TN; ++j) {
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
-        }
       }
       __builtin_amdgcn_sched_barrier(0);
     }

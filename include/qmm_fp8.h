@@ -109,7 +109,8 @@ int qmm_fp8(const void *w, size_t w_bytes, const float *w_scale, const void *x, 
  *                must equal rows.
  *   y            [rows][n] of y_type, 16-byte aligned; rows in no run (before
  *                offsets[0], from offsets[n_experts] on) are left as they were
- *   rows >= 0 (0: nothing is done), n, k as in qmm_fp8, 1 <= n_experts <= QMM_MAX_EXPERTS
+ *   rows >= 0 (0: nothing is done), n, k as in qmm_fp8, 1 <= n_experts <= QMM_MAX_EXPERTS;
+ *   with row_index, x must be under 4 GiB (QMV_ERR_RANGE)
  * offsets and row_index are read on the device. Offsets are clamped to
  * [0, rows]; where they decrease, which rows are written is not defined, but no
  * memory outside the arguments is touched. Needs no workspace.
