@@ -9,7 +9,6 @@ without a built library raises ImportError.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 
@@ -473,61 +472,79 @@ def qmv_stream_read(buf, grid: int = 1024, depth: int = 4, nontemporal: bool = F
 
 
 # ---------------------------------------------------------------- e4m3 and grouped products
+#
+# A decode step calls these between kernels of a few microseconds, so the checks
+# of a correct call are a handful of attribute reads; a refused one is explained
+# afterwards.
 
 def _blocks(k: int) -> int:
     return -(-k // 128)
 
 
-def _e4m3_types():
-    torch = _torch()
-    return (torch.float8_e4m3fn, torch.uint8)
+_F32 = (_torch().float32,)
+_I32 = (_torch().int32,)
+_U8 = (_torch().uint8,)
+_E4M3 = (_torch().float8_e4m3fn, _torch().uint8)
+_BF16 = _bf16_types()
+_FLOATS = {_torch().float32: 0, _torch().bfloat16: 1}   # QMM_F32, QMM_BF16
 
 
-def _float_type(t, name):
-    torch = _torch()
-    if t.dtype not in (torch.float32, torch.bfloat16):
-        raise TypeError(f"{name} has dtype {t.dtype}, expected float32 or bfloat16")
-    return 0 if t.dtype == torch.float32 else 1   # QMM_F32, QMM_BF16
-
-
-def _same_device(named):
-    first_name, first = named[0]
-    for name, t in named[1:]:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, {first_name} on {first.device}")
-
-
-def _shape(t, name, *shape):
+def _explain(t, name, types, shape, index):
+    _dev(t, name, types)
     if tuple(t.shape) != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    raise ValueError(f"{name} is on {t.device}, other tensors on cuda:{index}")
 
 
-def _on(device, stream):
-    """Makes the tensors' own device current for the C call; its current stream unless one is given."""
+def _take(t, name, types, shape, index):
+    """Device address of a contiguous tensor of one of `types` and of `shape` on device `index`."""
+    try:
+        if t.dtype in types and t.shape == shape and t.is_contiguous() and t.get_device() == index:   # host: -1
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _explain(t, name, types, shape, index)
+
+
+def _first(x, name, types, dims):
+    """Device index and shape of the tensor that the others go by."""
+    _dev(x, name, types)
+    if x.dim() != dims:
+        raise ValueError(f"{name} has {x.dim()} dimensions, expected {dims}")
+    return x.get_device(), x.shape
+
+
+def _run(fn, name, index, stream, *args):
+    """Calls the C entry point on the tensors' own device, on its current stream unless one is given."""
     torch = _torch()
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    if s.device != device:
-        raise ValueError(f"stream is on {s.device}, the tensors on {device}")
-    same = torch.cuda.current_device() == device.index
-    return contextlib.nullcontext() if same else torch.cuda.device(device), ctypes.c_void_p(s.cuda_stream)
+    if stream is None:
+        raw = torch._C._cuda_getCurrentRawStream(index)   # torch.cuda.current_stream(index) without its object
+    elif stream.device_index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+    else:
+        raw = stream.cuda_stream
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            rc = fn(*args, raw)
+    if rc:
+        raise QmvError(rc, name)
 
 
 def _quant(fn, name, x, gated, xq, xs, stream):
     torch = _torch()
-    _dev(x, "x", (torch.float32, torch.bfloat16))
-    if x.dim() != 2 or (gated and x.shape[1] % 2):
-        raise ValueError(f"{name}: x must be [m, {'2 k' if gated else 'k'}], got {tuple(x.shape)}")
-    m, k = x.shape[0], x.shape[1] // (2 if gated else 1)
+    index, (m, k) = _first(x, "x", tuple(_FLOATS), 2)
+    if gated:
+        if k % 2:
+            raise ValueError(f"{name}: x must be [m, 2 k], got {(m, k)}")
+        k //= 2
     if xq is None:
         xq = torch.empty((m, k), dtype=torch.float8_e4m3fn, device=x.device)
     if xs is None:
         xs = torch.empty((_blocks(k), m), dtype=torch.float32, device=x.device)
-    _shape(_dev(xq, "xq", _e4m3_types()), "xq", m, k)
-    _shape(_dev(xs, "xs", (torch.float32,)), "xs", _blocks(k), m)
-    _same_device([("x", x), ("xq", xq), ("xs", xs)])
-    guard, s = _on(x.device, stream)
-    with guard:
-        _check(fn(_ptr(x), _float_type(x, "x"), _ptr(xq), _ptr(xs), m, k, s), name)
+    _run(fn, name, index, stream, x.data_ptr(), _FLOATS[x.dtype], _take(xq, "xq", _E4M3, (m, k), index),
+         _take(xs, "xs", _F32, (_blocks(k), m), index), m, k)
     return xq, xs
 
 
@@ -543,18 +560,15 @@ def qmm_fp8_quant_silu_mul(x, xq=None, xs=None, stream=None):
 
 def qmm_fp8_workspace(m: int, n: int, k: int, out_dtype=None) -> int:
     """Bytes of ws a qmm_fp8 call of this shape needs (y fp32 unless out_dtype says bf16)."""
-    torch = _torch()
-    return lib.qmm_fp8_workspace(m, n, k, 0 if out_dtype in (None, torch.float32) else 1)
+    return lib.qmm_fp8_workspace(m, n, k, 0 if out_dtype is None else _FLOATS[out_dtype])
 
 
-def _y(y, rows, n, out_dtype, device):
-    torch = _torch()
-    if y is None:
-        y = torch.empty((rows, n), dtype=out_dtype or torch.float32, device=device)
+def _y_type(y, out_dtype):
+    if y.dtype not in _FLOATS:
+        raise TypeError(f"y has dtype {y.dtype}, expected float32 or bfloat16")
     if out_dtype is not None and y.dtype != out_dtype:
         raise TypeError(f"y has dtype {y.dtype}, out_dtype is {out_dtype}")
-    _shape(_dev(y, "y", None), "y", rows, n)
-    return y, _float_type(y, "y")
+    return _FLOATS[y.dtype]
 
 
 def qmm_fp8(w, w_scale, x, x_scale, n: int, k: int, y=None, out_dtype=None, ws=None, stream=None):
@@ -565,64 +579,46 @@ def qmm_fp8(w, w_scale, x, x_scale, n: int, k: int, y=None, out_dtype=None, ws=N
     tensor of at least qmm_fp8_workspace(m, n, k, y.dtype) bytes to reuse.
     """
     torch = _torch()
-    _shape(_dev(w, "w", _e4m3_types()), "w", n, k)
-    _shape(_dev(w_scale, "w_scale", (torch.float32,)), "w_scale", _blocks(n), _blocks(k))
-    _dev(x, "x", _e4m3_types())
-    m = x.shape[0]
-    _shape(x, "x", m, k)
-    _shape(_dev(x_scale, "x_scale", (torch.float32,)), "x_scale", _blocks(k), m)
-    y, y_type = _y(y, m, n, out_dtype, x.device)
-    guard, s = _on(x.device, stream)
-    with guard:
-        if ws is None:
-            need = lib.qmm_fp8_workspace(m, n, k, y_type)
-            if need:
-                with torch.cuda.stream(stream):
-                    ws = torch.empty(need, dtype=torch.uint8, device=x.device)
-        else:
-            _dev(ws, "ws", (torch.uint8,))
-        _same_device([("x", x), ("w", w), ("w_scale", w_scale), ("x_scale", x_scale), ("y", y), ("ws", ws)])
-        _check(lib.qmm_fp8(_ptr(w), _nbytes(w), _ptr(w_scale), _ptr(x), _ptr(x_scale), _ptr(y), y_type, m, n, k,
-                           _ptr(ws), _nbytes(ws), s), "qmm_fp8")
+    index, (m, _) = _first(x, "x", _E4M3, 2)
+    if y is None:
+        y = torch.empty((m, n), dtype=out_dtype or torch.float32, device=x.device)
+    y_type = _y_type(y, out_dtype)
+    if ws is None:
+        need = lib.qmm_fp8_workspace(m, n, k, y_type)
+        if need:
+            with torch.cuda.stream(stream):
+                ws = torch.empty(need, dtype=torch.uint8, device=x.device)
+    _run(lib.qmm_fp8, "qmm_fp8", index, stream,
+         _take(w, "w", _E4M3, (n, k), index), n * k, _take(w_scale, "w_scale", _F32, (_blocks(n), _blocks(k)), index),
+         _take(x, "x", _E4M3, (m, k), index), _take(x_scale, "x_scale", _F32, (_blocks(k), m), index),
+         _take(y, "y", _FLOATS, (m, n), index), y_type, m, n, k,
+         None if ws is None else _take(ws, "ws", _U8, ws.shape, index), 0 if ws is None else ws.numel())
     return y
 
 
-def _grouped(name, w, w_scale, x, x_scale, offsets, n, k, row_index, y, out_dtype, stream):
+def _grouped(fn, name, types, w, w_scale, x, x_scale, offsets, n, k, row_index, y, out_dtype, stream):
     torch = _torch()
-    fp8 = w_scale is not None
-    types = _e4m3_types() if fp8 else _bf16_types()
-    _dev(w, "w", types)
-    e = w.shape[0]
-    _shape(w, "w", e, n, k)
-    _dev(x, "x", types)
-    x_rows = x.shape[0]
-    _shape(x, "x", x_rows, k)
-    if fp8:
-        _shape(_dev(w_scale, "w_scale", (torch.float32,)), "w_scale", e, _blocks(n), _blocks(k))
-        _shape(_dev(x_scale, "x_scale", (torch.float32,)), "x_scale", _blocks(k), x_rows)
-    _shape(_dev(offsets, "offsets", (torch.int32,)), "offsets", e + 1)
+    index, (x_rows, _) = _first(x, "x", types, 2)
+    _, (e, _, _) = _first(w, "w", types, 3)
     rows = x_rows
+    found = None
     if row_index is not None:
         rows = row_index.numel()
-        _shape(_dev(row_index, "row_index", (torch.int32,)), "row_index", rows)
+        found = _take(row_index, "row_index", _I32, (rows,), index)
     if y is None:
         # rows that belong to no expert are not written: zeros there rather than what the memory held
         with torch.cuda.stream(stream):
             y = torch.zeros((rows, n), dtype=out_dtype or torch.float32, device=x.device)
-    y, y_type = _y(y, rows, n, out_dtype, x.device)
-    if rows == 0:
-        return y
-    _same_device([("x", x), ("w", w), ("w_scale", w_scale), ("x_scale", x_scale), ("offsets", offsets),
-                  ("row_index", row_index), ("y", y)])
-    guard, s = _on(x.device, stream)
-    with guard:
-        if fp8:
-            rc = lib.qmm_fp8_grouped(_ptr(w), _nbytes(w), _ptr(w_scale), _ptr(x), _ptr(x_scale), _ptr(offsets),
-                                     _ptr(row_index), _ptr(y), y_type, rows, x_rows, n, k, e, s)
-        else:
-            rc = lib.qmm_bf16_grouped(_ptr(w), _nbytes(w), _ptr(x), _ptr(offsets), _ptr(row_index), _ptr(y), y_type,
-                                      rows, x_rows, n, k, e, s)
-    _check(rc, name)
+    y_type = _y_type(y, out_dtype)
+    wp, xp = _take(w, "w", types, (e, n, k), index), _take(x, "x", types, (x_rows, k), index)
+    op, yp = _take(offsets, "offsets", _I32, (e + 1,), index), _take(y, "y", _FLOATS, (rows, n), index)
+    if types is _E4M3:
+        wsp = _take(w_scale, "w_scale", _F32, (e, _blocks(n), _blocks(k)), index)
+        xsp = _take(x_scale, "x_scale", _F32, (_blocks(k), x_rows), index)
+        if rows:
+            _run(fn, name, index, stream, wp, e * n * k, wsp, xp, xsp, op, found, yp, y_type, rows, x_rows, n, k, e)
+    elif rows:
+        _run(fn, name, index, stream, wp, 2 * e * n * k, xp, op, found, yp, y_type, rows, x_rows, n, k, e)
     return y
 
 
@@ -634,11 +630,11 @@ def qmm_fp8_grouped(w, w_scale, x, x_scale, offsets, n: int, k: int, row_index=N
     row_index (int32, one per row of y): the row of x to take, outside x for a row of zeros; None: the same row.
     Rows of y that belong to no expert are left as they were (zeros when y is None).
     """
-    if w_scale is None:
-        raise TypeError("w_scale must be a torch tensor")
-    return _grouped("qmm_fp8_grouped", w, w_scale, x, x_scale, offsets, n, k, row_index, y, out_dtype, stream)
+    return _grouped(lib.qmm_fp8_grouped, "qmm_fp8_grouped", _E4M3, w, w_scale, x, x_scale, offsets, n, k, row_index, y,
+                    out_dtype, stream)
 
 
 def qmm_bf16_grouped(w, x, offsets, n: int, k: int, row_index=None, y=None, out_dtype=None, stream=None):
     """As qmm_fp8_grouped on bf16 w [experts, n, k] and x [x_rows, k]."""
-    return _grouped("qmm_bf16_grouped", w, None, x, None, offsets, n, k, row_index, y, out_dtype, stream)
+    return _grouped(lib.qmm_bf16_grouped, "qmm_bf16_grouped", _BF16, w, None, x, None, offsets, n, k, row_index, y,
+                    out_dtype, stream)
