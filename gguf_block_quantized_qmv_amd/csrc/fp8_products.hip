@@ -465,58 +465,64 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
 #pragma unroll
     for (int j = 0; j < S::TN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
-  // One block: the wave's weight operands stay, the rows of x pass one 16-row
-  // tile after the other. A tile's products are added one tile later, so that
-  // the fma of one run beside the matrix instructions of the next. With
-  // next_too the loads of the next block (a whole one) go out over the first half.
+  // One block: the wave's weight operands stay in registers, the rows of x pass
+  // one 16-row tile after the other, and a tile's products are added one tile
+  // later, so that the fma run beside the matrix instructions. The last tile of
+  // a block is multiplied after the barrier, each weight operand making room for
+  // the next block's as it is used: the matrix cores have work while the first
+  // reads of a stage are under way. With next_too the loads of the next block (a
+  // whole one) go out over the first half.
+  Operand<KIND> wf[S::TN], xf[2];   // xf[1] between blocks: the last tile of the block before
+  v4f d[2][S::TN];                  // d[0] between blocks: the products of the tile before that
+  float s[2] = {0.0f, 0.0f};        // scales of the tiles in xf[1] and d[0]: s[1], s[0]
+  float ws_before = 0.0f;
+  static_assert(S::TM % 2 == 0, "tiles alternate between two registers");
+  {
+    const Frag none = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+    xf[1].set(none);
+#pragma unroll
+    for (int j = 0; j < S::TN; ++j) {
+      wf[j].set(none);
+      d[0][j] = kZero4;
+    }
+  }
   auto compute = [&](auto next_too, int b, float ws, const uint8_t *stage, const float *scale, uint8_t *next, float *next_scale) {
-#ifndef VEVERY
-#define VEVERY ((S::kLoads + (S::TM + 1) / 2 - 1) / ((S::TM + 1) / 2))
-#endif
-    constexpr int kEvery = VEVERY;
+    constexpr int kEvery = (S::kLoads + (S::TM + 1) / 2 - 1) / ((S::TM + 1) / 2);
     auto read = [&](int lo, int hi, int rows16, Operand<KIND> &to) {
       Frag f;
       f.lo = *reinterpret_cast<const v4i *>(stage + lo + rows16 * 2048);
       f.hi = *reinterpret_cast<const v4i *>(stage + hi + rows16 * 2048);
       to.set(f);
     };
-    Operand<KIND> wf[S::TN], xf[2];
-    float s[2];
-    v4f d[2][S::TN];
-    if constexpr (FP8) s[0] = scale[wm * S::TM * 16 + r];
-    read(x_at, x_at ^ 64, 0, xf[0]);
 #pragma unroll
-    for (int j = 0; j < S::TN; ++j) read(w_at, w_at ^ 64, j, wf[j]);
-#pragma unroll
-    for (int i = 0; i < S::TM; ++i) {
-      const float before = i > 0 ? s[(i - 1) & 1] * ws : 0.0f;
-      if (i + 1 < S::TM) {
-        if constexpr (FP8) s[(i + 1) & 1] = scale[(wm * S::TM + i + 1) * 16 + r];
-        read(x_at, x_at ^ 64, i + 1, xf[(i + 1) & 1]);
-      }
+    for (int i = -1; i < S::TM - 1; ++i) {
+      // i = -1: the last tile of the block before
+      constexpr int kLast = S::TM - 1;
+      const int now = i & 1, then = now ^ 1;                 // buffers of this tile and of its neighbours
+      const int tile = i < 0 ? kLast : i, back = i < 0 ? kLast - 1 : i == 0 ? kLast : i - 1;
+      const float before = s[then] * (i <= 0 ? ws_before : ws);
+      if constexpr (FP8) s[then] = scale[(wm * S::TM + i + 1) * 16 + r];
+      read(x_at, x_at ^ 64, i + 1, xf[then]);
       if constexpr (decltype(next_too)::value) {
-        if (i == 0) load_scales(b + 1, next_scale);
+        if (i < 0) load_scales(b + 1, next_scale);
 #pragma unroll
-        for (int l = i * kEvery; l < (i + 1) * kEvery && l < S::kLoads; ++l) load_piece(l, b + 1, next, false);
+        for (int l = (i + 1) * kEvery; l < (i + 2) * kEvery && l < S::kLoads; ++l) load_piece(l, b + 1, next, false);
       }
-      if constexpr (FP8) {
 #pragma unroll
-        for (int j = 0; j < S::TN; ++j) {
-          d[i & 1][j] = mma_block<KIND>(wf[j], xf[i & 1], kZero4);
-          if (i > 0) scaled_add(before, d[(i - 1) & 1][j], acc[i > 0 ? i - 1 : 0][j]);
-          // keeps the fma of a result TN matrix instructions behind it
-          if (KIND == kNative) __builtin_amdgcn_sched_barrier(0);
+      for (int j = 0; j < S::TN; ++j) {
+        if constexpr (FP8) {
+          d[now][j] = mma_block<KIND>(wf[j], xf[now], kZero4);
+          scaled_add(before, d[then][j], acc[back][j]);
+        } else {
+          acc[tile][j] = mma_block<KIND>(wf[j], xf[now], acc[tile][j]);
         }
-      } else {
-#pragma unroll
-        for (int j = 0; j < S::TN; ++j) acc[i][j] = mma_block<KIND>(wf[j], xf[i & 1], acc[i][j]);
+        if (i < 0) read(w_at, w_at ^ 64, j, wf[j]);
+        // keeps the fma of a result TN matrix instructions behind it
+        if (KIND == kNative) __builtin_amdgcn_sched_barrier(0);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
-    if constexpr (FP8) {
-#pragma unroll
-      for (int j = 0; j < S::TN; ++j) scaled_add(s[(S::TM - 1) & 1] * ws, d[(S::TM - 1) & 1][j], acc[S::TM - 1][j]);
-    }
+    ws_before = ws;
   };
 
   issue(blk0, stage0, scale0);
@@ -542,6 +548,17 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
     if (left > 2) {
       stage_barrier();
       compute(std::false_type{}, b + 2, ws2, stage0, scale0, nullptr, nullptr);
+    }
+  }
+
+  // the last tile of the last block
+#pragma unroll
+  for (int j = 0; j < S::TN; ++j) {
+    if constexpr (FP8) {
+      scaled_add(s[0] * ws_before, d[0][j], acc[S::TM - 2][j]);
+      scaled_add(s[1] * ws_before, mma_block<KIND>(wf[j], xf[1], kZero4), acc[S::TM - 1][j]);
+    } else {
+      acc[S::TM - 1][j] = mma_block<KIND>(wf[j], xf[1], acc[S::TM - 1][j]);
     }
   }
 
