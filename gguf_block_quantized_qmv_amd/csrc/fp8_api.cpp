@@ -59,7 +59,7 @@ int grouped(const void *w, size_t w_bytes, const float *w_scale, const void *x, 
   const size_t wb = (size_t)n_experts * n * k * value_bytes;   // <= 2^51
   if (w_bytes != wb) return QMV_ERR_SIZE;
   if (rows == 0) return QMV_OK;
-  if (!qmv::fp8::grouped_fits_grid(rows, n, n_experts)) return QMV_ERR_RANGE;
+  if (!qmv::fp8::grouped_fits_grid(rows, n, n_experts, e4m3 && y_type == QMM_F32)) return QMV_ERR_RANGE;
   // rows are gathered by 32-bit byte offsets
   if (row_index && (size_t)x_rows * k * value_bytes > UINT32_MAX) return QMV_ERR_RANGE;
   // with no row of x every index is out of range, and x itself may be null
@@ -78,9 +78,8 @@ int grouped(const void *w, size_t w_bytes, const float *w_scale, const void *x, 
   qmv::ProductArgs a{};
   a.w = static_cast<const uint8_t *>(w);
   a.w_scale = w_scale;
-  // with no row of x, the kernels read a weight row in its place and store zeros
-  a.x = static_cast<const uint8_t *>(x_rows > 0 ? x : w);
-  a.x_scale = x_rows > 0 ? x_scale : w_scale;
+  a.x = static_cast<const uint8_t *>(x);
+  a.x_scale = x_scale;
   a.offsets = offsets;
   a.index = row_index;
   a.y = y;

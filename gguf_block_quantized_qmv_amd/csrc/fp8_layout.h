@@ -19,11 +19,13 @@ constexpr int kSlots = 256;   // compute units a plan fills (a 256-CU MI355X)
 constexpr int blocks_of(int k) { return (k + kBlock - 1) / kBlock; }
 constexpr int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
+constexpr int kLdsPerCu = 160 * 1024;
+
 // ---- tile shapes (rows of x by rows of w of one workgroup) -------------------
 
-enum Tile { kTile32 = 0, kTile64 = 1, kTile128 = 2, kTile256 = 3 };
+enum Tile { kTile32 = 0, kTile64 = 1, kTile128 = 2, kTile256 = 3, kTile256Wide = 4 };
 constexpr int tile_rows(int t) { return t == kTile32 ? 32 : t == kTile64 ? 64 : t == kTile128 ? 128 : 256; }
-constexpr int tile_cols(int t) { return t == kTile256 ? 256 : 128; }
+constexpr int tile_cols(int t) { return t == kTile32 ? 64 : t == kTile256Wide ? 256 : 128; }
 
 // ---- dense -------------------------------------------------------------------
 
@@ -61,19 +63,23 @@ inline StreamPlan stream_plan(int n, int nb, int slots) {
 }
 
 inline DensePlan dense_plan(int m, int n, int k, bool y_bf16) {
-  DensePlan p{m <= QMM_SAME_ROWS, kTile128, 1};
-  if (p.stream) return p;
-  p.tile = m <= 32 ? kTile32 : m <= 64 ? kTile64 : kTile128;
-  const int64_t big = (int64_t)ceil_div(m, 256) * ceil_div(n, 256);
-  if (y_bf16 && m > 128 && big >= kSlots) p.tile = kTile256;
-  const int64_t tiles = (int64_t)ceil_div(m, tile_rows(p.tile)) * ceil_div(n, tile_cols(p.tile));
+  DensePlan p{false, kTile128, 1};
   const int nb = blocks_of(k);
-  if (tiles < 2 * kSlots && p.tile != kTile256) {
-    int64_t s = 2 * kSlots / tiles;
-    if (s > nb / 4) s = nb / 4;      // at least four blocks a part
-    if (s > 16) s = 16;
-    p.splits = s < 1 ? 1 : (int)s;
+  if (m <= 32) {
+    // by (n, k) alone
+    p.tile = kTile32;
+    p.stream = (int64_t)n * k < (int64_t)32 << 20;
+    if (p.stream) return p;
+  } else {
+    p.tile = m <= 64 ? kTile64 : m <= 128 ? kTile128 : kTile256;
+    const int64_t wide = (int64_t)ceil_div(m, 256) * ceil_div(n, 256);
+    if (y_bf16 && m > 128 && wide >= kSlots) p.tile = kTile256Wide;
   }
+  const int64_t tiles = (int64_t)(m <= 32 ? 1 : ceil_div(m, tile_rows(p.tile))) * ceil_div(n, tile_cols(p.tile));
+  int64_t s = kSlots / tiles;
+  if (s > nb / 4) s = nb / 4;      // at least four blocks a part
+  if (s > 16) s = 16;
+  p.splits = s < 1 ? 1 : (int)s;
   return p;
 }
 
@@ -91,10 +97,16 @@ struct GroupedPlan {
   int tile;
 };
 
-inline GroupedPlan grouped_plan(int rows, int n_experts) {
+inline GroupedPlan grouped_plan(int rows, int n_experts, bool exact) {
   const int avg = rows / (n_experts < 1 ? 1 : n_experts);
-  GroupedPlan p{avg <= 4, kTile32};
-  p.tile = avg <= 32 ? kTile32 : avg <= 64 ? kTile64 : kTile128;
+#ifndef GSTREAM
+#define GSTREAM 0
+#endif
+#ifndef GBIG
+#define GBIG kTile256
+#endif
+  GroupedPlan p{rows <= GSTREAM, kTile32};
+  p.tile = avg <= 24 ? kTile32 : avg <= 64 ? kTile64 : avg <= 128 ? kTile128 : exact ? kTile256 : GBIG;
   return p;
 }
 
@@ -112,8 +124,8 @@ inline bool dense_fits_grid(int m, int n, int k, bool y_bf16) {
   return p.stream || (int64_t)ceil_div(m, tile_rows(p.tile)) * ceil_div(n, tile_cols(p.tile)) * p.splits <= kMaxWorkgroups;
 }
 
-inline bool grouped_fits_grid(int rows, int n, int n_experts) {
-  const GroupedPlan p = grouped_plan(rows, n_experts);
+inline bool grouped_fits_grid(int rows, int n, int n_experts, bool exact) {
+  const GroupedPlan p = grouped_plan(rows, n_experts, exact);
   return p.stream || grouped_row_tiles(rows, n_experts, tile_rows(p.tile)) * ceil_div(n, tile_cols(p.tile)) <= kMaxWorkgroups;
 }
 

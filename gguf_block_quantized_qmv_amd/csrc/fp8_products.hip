@@ -182,7 +182,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
 
   for (int t0 = begin; t0 < end; t0 += 16) {
     int src;
-    source_row(p, t0 + r < end ? t0 + r : end - 1, src);
+    const bool in_x = source_row(p, t0 + r < end ? t0 + r : end - 1, src);   // else a row of zeros
     using Offset = std::conditional_t<GROUPED, uint64_t, uint32_t>;   // dense: within 16 rows
     Offset xlane = (Offset)src * (Offset)p.k_bytes + (Offset)(g * 16);
     uint32_t xslane = (uint32_t)src;
@@ -195,7 +195,9 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
       if constexpr (FP8) {
         asm("" : "+v"(xslane), "+v"(wslane));
         const float *zeros = reinterpret_cast<const float *>(g_zeros);
-        xs[u] = (ok ? p.x_scale + (size_t)b * p.x_rows : zeros)[ok ? xslane : 0];
+        const float *x = (ok ? p.x_scale + (size_t)b * p.x_rows : zeros) + (ok ? xslane : 0);
+        if (GROUPED) x = in_x ? x : zeros;
+        xs[u] = *x;
         ws[u] = (ok ? wsbase + b : zeros)[ok ? wslane : 0];
       }
     };
@@ -205,6 +207,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
       const uint8_t *zeros = reinterpret_cast<const uint8_t *>(g_zeros);
       const uint8_t *w = (ok ? wbase + (size_t)b * 128 : zeros) + (ok ? wlane : 0);
       const uint8_t *x = (ok ? p.x + (size_t)b * 128 : zeros) + (ok ? xlane : 0);
+      if (GROUPED) x = in_x ? x : zeros;
       wf[u].lo = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(w));
       wf[u].hi = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(w + 64));
       xf[u].lo = *reinterpret_cast<const v4i *>(x);
@@ -236,11 +239,11 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
       const uint8_t *w = wbase + (size_t)whole * 128 + wlane, *x = p.x + (size_t)whole * 128 + xlane;
       if (g * 16 < tail) {
         wf[0].lo = *reinterpret_cast<const v4i *>(w);
-        xf[0].lo = *reinterpret_cast<const v4i *>(x);
+        if (in_x) xf[0].lo = *reinterpret_cast<const v4i *>(x);
       }
       if (g * 16 + 64 < tail) {
         wf[0].hi = *reinterpret_cast<const v4i *>(w + 64);
-        xf[0].hi = *reinterpret_cast<const v4i *>(x + 64);
+        if (in_x) xf[0].hi = *reinterpret_cast<const v4i *>(x + 64);
       }
       load_scales(whole, 0, true);
       use(0);
@@ -253,10 +256,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
       float sum = red[0][threadIdx.x];
 #pragma unroll
       for (int v = 1; v < NW; ++v) sum += red[v][threadIdx.x];
-      if (row < end && col < n1) {
-        int at;
-        store_y(p, row, col, source_row(p, row, at) ? sum : 0.0f);
-      }
+      if (row < end && col < n1) store_y(p, row, col, sum);
     }
     __syncthreads();
   }
@@ -264,24 +264,41 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
 
 // ---- many rows: tiles through LDS --------------------------------------------------
 //
-// A workgroup owns BM rows of x by BN rows of w. Each step moves one block of
-// k of both into one of two LDS stages by direct-to-LDS loads while the waves
-// multiply the other stage; one barrier a step hands the stages over. A stage
-// row is 128 bytes, eight 16-byte chunks; chunk c of row r sits at slot
-// c ^ ((r / 2) % 8), which leaves the fragment reads (16 consecutive rows, one
-// chunk) free of bank conflicts. The direct loads write LDS in lane order, so
-// the permutation is applied to the global address each lane reads.
+// A workgroup computes BM x BN tiles of y (rows of x by rows of w), one after
+// the other. Each step moves one block of k of both into an LDS stage by
+// direct-to-LDS loads, kStages - 1 blocks ahead of the waves, which multiply
+// the oldest stage; one barrier a step hands the stages on. The first blocks of
+// the next tile are sent before the results of a tile are stored, so that the
+// memory works through the stores.
+//
+// A stage row is 128 bytes, eight 16-byte chunks. A fragment read takes one
+// chunk of 16 rows; it is free of bank conflicts when the eight even and the
+// eight odd rows each find the chunk in eight different slots: chunk c of row r
+// sits at slot c ^ f(r). The direct loads write LDS in lane order, so the
+// permutation is applied to the global address each lane reads.
+//  * rows of x: a fragment is 16 consecutive rows, f(r) = r / 2 % 8;
+//  * rows of w, where a wave has an even number of column tiles: two tiles share
+//    32 rows in alternating fours, so that a lane's two results of four columns
+//    are eight neighbouring ones (one 16-byte store in bf16); f(r) takes bits
+//    1, 3 and 4 of r.
 constexpr int kStageRow = 128;
 
-template <int BM_, int BN_, int WM_, int WN_>
+template <int BM_, int BN_, int WM_, int WN_, int STAGES_>
 struct Shape {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;   // waves along rows of x, of w
+  static constexpr int kStages = STAGES_;
   static constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
   static constexpr int TM = BM / WM / 16, TN = BN / WN / 16;     // MFMA tiles of a wave
+  static constexpr bool kPairs = TN % 2 == 0;
   static constexpr int kLoads = (BM + BN) / 8 / kWaves;          // 1 KiB direct loads of a wave and step
   static constexpr int kStageBytes = (BM + BN) * kStageRow;
+  static constexpr int kScales = (BM + 63) / 64 * 64;
+  static constexpr int kLdsBytes = kStages * (kStageBytes + kScales * 4);
+  static constexpr int kPerCu = fp8::kLdsPerCu / kLdsBytes;      // workgroups a CU holds
   static_assert((BM + BN) % (8 * kWaves) == 0 && TM * WM * 16 == BM && TN * WN * 16 == BN, "whole tiles and loads");
   static_assert(BN / WN <= 128 && 128 % (BN / WN) == 0, "a wave's columns lie under one weight scale");
+  static_assert(TM % 2 == 0, "tiles alternate between two registers");
+  static_assert(kStages >= 2 && kStages <= 4 && kPerCu >= 1, "the arrays below");
 };
 
 // Buffer form of the direct load: LDS at `to` + 16 (or 4) bytes a lane gets
@@ -291,315 +308,406 @@ typedef __amdgpu_buffer_rsrc_t Buffer;
 __device__ __forceinline__ Buffer buffer_of(const void *base, uint32_t size) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), 0, (int)size, 0x00020000);
 }
-constexpr uint32_t kOutside = 0xFFFFFFFFu;   // an offset past every buffer
+constexpr uint32_t kOutside = 0xFFFFFFF0u;   // an offset past every buffer
 __device__ __forceinline__ void load_lds16(Buffer from, uint32_t at, uint32_t step, void *to) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void *)to, 16, (int)at, (int)step,
                                            0, 0);
 }
-__device__ __forceinline__ void load_lds4(Buffer from, uint32_t at, uint32_t step, void *to) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void *)to, 4, (int)at, (int)step,
-                                           0, 0);
+__device__ __forceinline__ void load_lds4(Buffer from, uint32_t at, void *to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void *)to, 4, (int)at, 0, 0, 0);
 }
 
-// Every direct load of this wave has landed and every LDS read has returned,
-// then all waves meet.
+// All but the last `AFTER` memory operations of this wave are done and every
+// LDS read has returned, then all waves meet. (Loads and stores of a wave are
+// counted off in order.)
+template <int AFTER>
 __device__ __forceinline__ void stage_barrier() {
+  static_assert(AFTER < 64, "the counter's range");
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0) lgkmcnt(0)
+  __builtin_amdgcn_s_waitcnt((AFTER & 15) | (AFTER >> 4) << 14 | 0x0070);   // vmcnt(AFTER) lgkmcnt(0)
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
-}
-
-// id -> position in an order that gives each of the eight XCDs (workgroups are
-// dealt to them in turn) one contiguous run of [0, total).
-__device__ __forceinline__ int xcd_order(int id, int total) {
-  const int q = total >> 3, rest = total & 7, x = id & 7;
-  return x * q + (x < rest ? x : rest) + (id >> 3);
 }
 
 template <class S, Kind KIND, bool GROUPED>
 __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const ProductArgs p) {
   constexpr bool FP8 = is_e4m3(KIND);
-  __shared__ __attribute__((aligned(1024))) uint8_t stage0[S::kStageBytes];
-  __shared__ __attribute__((aligned(1024))) uint8_t stage1[S::kStageBytes];
-  __shared__ float scale0[(S::BM + 63) / 64 * 64], scale1[(S::BM + 63) / 64 * 64];
-  const int lane = (int)threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  // one array a stage, each named in the unrolled loop below: the compiler then
+  // knows which reads a load in flight cannot touch
+  __shared__ __attribute__((aligned(1024))) uint8_t stage0[S::kStageBytes], stage1[S::kStageBytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t stage2[S::kStages > 2 ? S::kStageBytes : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t stage3[S::kStages > 3 ? S::kStageBytes : 16];
+  __shared__ float scale0[S::kScales], scale1[S::kScales], scale2[S::kStages > 2 ? S::kScales : 1],
+      scale3[S::kStages > 3 ? S::kScales : 1];
+  const int lane = (int)threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
   const int n_tiles = fp8::ceil_div(p.n, S::BN);
 
-  // this workgroup's tile
-  int expert = 0, m0, begin = 0, end = p.rows, nt, part = 0;
+  // tiles in all; grouped: the row tiles of each lane's run of experts, and
+  // their running sum over the lanes
+  const int per = fp8::ceil_div(p.n_experts, 64);
+  int total, mine = 0, upto = 0;
   if constexpr (GROUPED) {
-    // row tiles of each lane's run of experts, and their running sum over the lanes
-    const int per = fp8::ceil_div(p.n_experts, 64), e0 = lane * per;
-    int mine = 0;
-    for (int e = e0; e < e0 + per && e < p.n_experts; ++e) {
+    for (int e = lane * per; e < lane * per + per && e < p.n_experts; ++e) {
       int b0, b1;
       expert_rows(p.offsets, e, p.rows, b0, b1);
       mine += fp8::ceil_div(b1 - b0, S::BM);
     }
-    int upto = mine;
+    upto = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int o = __shfl_up(upto, d);
       if (lane >= d) upto += o;
     }
-    const int total = __builtin_amdgcn_readfirstlane(__shfl(upto, 63));
-    // decreasing offsets can give more tiles than the grid holds: they are not done
-    const int all = total < (int)gridDim.x / n_tiles ? total * n_tiles : (int)gridDim.x;
-    if ((int)blockIdx.x >= all) return;
-    const int id = xcd_order((int)blockIdx.x, all);
-    const int mt = id / n_tiles;
-    nt = id - mt * n_tiles;
-    const int owner = __ffsll((unsigned long long)__ballot(upto > mt)) - 1;
-    int left = mt - __builtin_amdgcn_readfirstlane(__shfl(upto - mine, owner));
-    expert = owner * per;
-    for (;;) {
-      expert_rows(p.offsets, expert, p.rows, begin, end);
-      const int t = fp8::ceil_div(end - begin, S::BM);
-      if (left < t) break;
-      left -= t;
-      ++expert;
-    }
-    expert = __builtin_amdgcn_readfirstlane(expert);
-    m0 = begin + left * S::BM;
+    // decreasing offsets can give more row tiles than rows and experts allow:
+    // the host has checked n_tiles times this bound
+    const int rows_most = p.rows / S::BM + (p.rows < p.n_experts ? p.rows : p.n_experts);
+    const int sum = uniform(__shfl(upto, 63));
+    total = (sum < rows_most ? sum : rows_most) * n_tiles;
   } else {
-    const int m_tiles = fp8::ceil_div(p.rows, S::BM);
-    const int tiles = m_tiles * n_tiles;
-    int id = xcd_order((int)blockIdx.x, tiles * p.splits);
-    part = id / tiles;
-    id -= part * tiles;
-    // bands of eight row tiles, rows first within a band
-    const int band = id / (8 * n_tiles), in = id - band * 8 * n_tiles;
-    const int high = m_tiles - band * 8 < 8 ? m_tiles - band * 8 : 8;
-    nt = in / high;
-    m0 = (band * 8 + in - nt * high) * S::BM;
+    total = fp8::ceil_div(p.rows, S::BM) * n_tiles * p.splits;
   }
-  // uniform, but divided on vector lanes: into scalar registers
-  m0 = uniform(m0);
-  nt = uniform(nt);
-  begin = uniform(begin);
-  end = uniform(end);
-  const int n0 = nt * S::BN;
-  const int blk0 = GROUPED ? 0 : uniform((int)((int64_t)p.nb * part / p.splits));
-  const int blk1 = GROUPED ? p.nb : uniform((int)((int64_t)p.nb * (part + 1) / p.splits));
+  // Workgroups are dealt to the eight XCDs in turn. Each XCD takes one
+  // contiguous run of the tiles, its workgroups side by side in it, so that
+  // neighbouring tiles share rows of x and w in the XCD's cache.
+  const int xcd = (int)blockIdx.x & 7, share = total >> 3, rest = total & 7;
+  const int first = xcd * share + (xcd < rest ? xcd : rest), count = share + (xcd < rest);
+  const int stride = ((int)gridDim.x - xcd + 7) >> 3;
+  int at = (int)blockIdx.x >> 3;
+  if (at >= count) return;
 
-  // This lane's direct loads: row q * 8 + lane / 8 of the stage, chunk by the
-  // slot, as an offset from a scalar base: the tile's first row of w, and of x
-  // unless its rows are gathered (from all of x, which the host then keeps under
-  // 4 GiB).
+  struct Tile {
+    int expert, m0, end, n0, part, blk0, blk1;
+  };
+  auto locate = [&](int id) {
+    Tile t{0, 0, p.rows, 0, 0, 0, p.nb};
+    if constexpr (GROUPED) {
+      const int mt = uniform(id / n_tiles);
+      t.n0 = (id - mt * n_tiles) * S::BN;
+      const int owner = uniform(__ffsll((unsigned long long)__ballot(upto > mt)) - 1);
+      int left = mt - uniform(__shfl(upto - mine, owner)), begin;
+      int e = owner * per;
+      for (;; ++e) {
+        expert_rows(p.offsets, e, p.rows, begin, t.end);
+        const int tiles = fp8::ceil_div(t.end - begin, S::BM);
+        if (left < tiles || e + 1 >= p.n_experts) break;
+        left -= tiles;
+      }
+      t.expert = uniform(e);
+      t.m0 = uniform(begin + left * S::BM);
+      t.end = uniform(t.end);
+    } else {
+      const int m_tiles = fp8::ceil_div(p.rows, S::BM), tiles = m_tiles * n_tiles;
+      t.part = uniform(id / tiles);
+      id -= t.part * tiles;
+      // bands of eight row tiles, rows first within a band
+      const int band = uniform(id / (8 * n_tiles)), in = id - band * 8 * n_tiles;
+      const int high = m_tiles - band * 8 < 8 ? m_tiles - band * 8 : 8;
+      const int nt = uniform(in / high);
+      t.n0 = nt * S::BN;
+      t.m0 = (band * 8 + in - nt * high) * S::BM;
+      if (p.splits > 1) {
+        t.blk0 = uniform((int)((int64_t)p.nb * t.part / p.splits));
+        t.blk1 = uniform((int)((int64_t)p.nb * (t.part + 1) / p.splits));
+      }
+    }
+    return t;
+  };
+
+  // This lane's direct loads of a tile's block: row q * 8 + lane / 8 of the
+  // stage, chunk by the slot, as an offset from a scalar base: the tile's first
+  // row of w, and of x unless its rows are gathered (from all of x, which the
+  // host then keeps under 4 GiB). A gathered row outside x is a row of zeros.
+  struct Loads {
+    Buffer x, w;
+    uint32_t from[S::kLoads];
+    uint32_t scale_from;
+  };
   const bool gather = GROUPED && p.index;
-  const Buffer wbuf = buffer_of(p.w + ((size_t)expert * p.n + n0) * p.k_bytes,
-                                (uint32_t)(p.n - n0 < S::BN ? p.n - n0 : S::BN) * (uint32_t)p.k_bytes);
-  const int x_first = gather ? 0 : m0, x_count = gather ? p.x_rows : end - m0 < S::BM ? end - m0 : S::BM;
-  const Buffer xbuf = buffer_of(p.x + (size_t)x_first * p.k_bytes, (uint32_t)x_count * (uint32_t)p.k_bytes);
-  uint32_t from[S::kLoads];
-  int chunk_at[S::kLoads];
-  int src[S::kLoads];
+  auto chunk_of = [&](int i) {
+    const int q = wave * S::kLoads + i, row = q * 8 + (lane >> 3), wrow = row - S::BM;
+    const int f = q < S::BM / 8 || !S::kPairs ? row >> 1 & 7 : (wrow >> 1 & 1) | (wrow >> 3 & 3) << 1;
+    return ((lane & 7) ^ f) * 16;
+  };
+  constexpr int kScaleWaves = S::kScales / 64;   // waves past these bring the same scales again: no branch in the loop
+  const int scale_to = wave % kScaleWaves * 64;
+  auto loads_of = [&](const Tile &t) {
+    Loads l;
+    l.w = buffer_of(p.w + ((size_t)t.expert * p.n + t.n0) * p.k_bytes,
+                    (uint32_t)(p.n - t.n0 < S::BN ? p.n - t.n0 : S::BN) * (uint32_t)p.k_bytes);
+    const int x_first = gather ? 0 : t.m0, x_count = gather ? p.x_rows : t.end - t.m0 < S::BM ? t.end - t.m0 : S::BM;
+    l.x = buffer_of(p.x + (size_t)x_first * p.k_bytes, (uint32_t)x_count * (uint32_t)p.k_bytes);
+    int row[S::kLoads + 1];
 #pragma unroll
-  for (int i = 0; i < S::kLoads; ++i) {
-    const int row = (wave * S::kLoads + i) * 8 + (lane >> 3);
-    chunk_at[i] = ((lane & 7) ^ ((row >> 1) & 7)) * 16;
-    if (wave * S::kLoads + i < S::BM / 8)
-      src[i] = (m0 + row < end ? m0 + row : end - 1) - x_first;
-    else
-      src[i] = n0 + row - S::BM < p.n ? row - S::BM : p.n - 1 - n0;
-  }
-  if (gather) {   // all index loads before the first use
-    int found[S::kLoads];
+    for (int i = 0; i < S::kLoads; ++i) {
+      const int q = wave * S::kLoads + i, r = q * 8 + (lane >> 3);
+      row[i] = q < S::BM / 8 ? (t.m0 + r < t.end ? t.m0 + r : t.end - 1) - x_first
+                             : t.n0 + r - S::BM < p.n ? r - S::BM : p.n - 1 - t.n0;
+    }
+    row[S::kLoads] = t.m0 + scale_to + lane < t.end ? t.m0 + scale_to + lane : t.end - 1;
+    if (gather) {   // all index loads before the first use
+      int found[S::kLoads + 1];
 #pragma unroll
-    for (int i = 0; i < S::kLoads; ++i) found[i] = p.index[wave * S::kLoads + i < S::BM / 8 ? src[i] : m0];
+      for (int i = 0; i <= S::kLoads; ++i)
+        found[i] = p.index[i == S::kLoads || wave * S::kLoads + i < S::BM / 8 ? row[i] : t.m0];
 #pragma unroll
-    for (int i = 0; i < S::kLoads; ++i)
-      if (wave * S::kLoads + i < S::BM / 8) src[i] = (unsigned)found[i] < (unsigned)p.x_rows ? found[i] : 0;
-  }
+      for (int i = 0; i <= S::kLoads; ++i)
+        if (i == S::kLoads || wave * S::kLoads + i < S::BM / 8) row[i] = found[i];
+    }
 #pragma unroll
-  for (int i = 0; i < S::kLoads; ++i) from[i] = (uint32_t)src[i] * (uint32_t)p.k_bytes + (uint32_t)chunk_at[i];
-  // the scales of x, 64 rows a wave (waves past the tile's rows bring the same
-  // values again: no branch in the loop)
-  constexpr int kScaleRows = (S::BM + 63) / 64 * 64;
-  const int scale_to = wave * 64 % kScaleRows;
-  uint32_t scale_from = 0;
-  if constexpr (FP8) {
-    const int row = m0 + scale_to + lane;
-    int at;
-    source_row(p, row < end ? row : end - 1, at);
-    scale_from = (uint32_t)at * 4;
-  }
+    for (int i = 0; i < S::kLoads; ++i) {
+      l.from[i] = (uint32_t)row[i] * (uint32_t)p.k_bytes + (uint32_t)chunk_of(i);
+      if (gather && wave * S::kLoads + i < S::BM / 8 && (unsigned)row[i] >= (unsigned)p.x_rows) l.from[i] = kOutside;
+    }
+    l.scale_from = (unsigned)row[S::kLoads] < (unsigned)p.x_rows ? (uint32_t)row[S::kLoads] * 4 : kOutside;
+    return l;
+  };
   const int tail = p.k_bytes & 127;   // bytes of a partial last block
   // one of the wave's direct loads of block b
-  auto load_piece = [&](int i, int b, uint8_t *stage, bool last) {
-    const uint32_t at = last && chunk_at[i] >= tail ? kOutside : from[i];
+  auto load_piece = [&](const Loads &l, int i, int b, uint8_t *stage, bool last) {
+    const uint32_t from = last && chunk_of(i) >= tail ? kOutside : l.from[i];
     uint8_t *to = stage + (wave * S::kLoads + i) * 1024;
+    // kOutside stays outside: the hardware compares the offset without the scalar step
     if (wave * S::kLoads + i < S::BM / 8)
-      load_lds16(xbuf, at, (uint32_t)b * 128, to);
+      load_lds16(l.x, from, (uint32_t)b * 128, to);
     else
-      load_lds16(wbuf, at, (uint32_t)b * 128, to);
+      load_lds16(l.w, from, (uint32_t)b * 128, to);
   };
-  auto load_scales = [&](int b, float *scale) {
+  auto load_scales = [&](const Loads &l, int b, float *scale) {
     if constexpr (FP8)
-      load_lds4(buffer_of(p.x_scale + (size_t)b * p.x_rows, (uint32_t)p.x_rows * 4), scale_from, 0, scale + scale_to);
+      load_lds4(buffer_of(p.x_scale + (size_t)b * p.x_rows, (uint32_t)p.x_rows * 4), l.scale_from, scale + scale_to);
   };
   // all loads of block b, which may be the partial last one
-  auto issue = [&](int b, uint8_t *stage, float *scale) {
+  auto issue = [&](const Loads &l, int b, uint8_t *stage, float *scale) {
     const bool partial = tail != 0 && b == p.nb - 1;
 #pragma unroll
-    for (int i = 0; i < S::kLoads; ++i) load_piece(i, b, stage, partial);
-    load_scales(b, scale);
+    for (int i = 0; i < S::kLoads; ++i) load_piece(l, i, b, stage, partial);
+    load_scales(l, b, scale);
+  };
+  // Block b of a tile in stage (b - blk0) % kStages; the loads of kAhead blocks
+  // are under way.
+  constexpr int kAhead = S::kStages - 1;
+  constexpr int kAfter = (kAhead - 1) * (S::kLoads + (FP8 ? 1 : 0));   // direct loads sent after a block's own
+  auto issue_first = [&](const Loads &l, const Tile &t) {
+    issue(l, t.blk0, stage0, scale0);
+    if constexpr (kAhead > 1) {
+      if (t.blk0 + 1 < t.blk1) issue(l, t.blk0 + 1, stage1, scale1);
+    }
+    if constexpr (kAhead > 2) {
+      if (t.blk0 + 2 < t.blk1) issue(l, t.blk0 + 2, stage2, scale2);
+    }
+  };
+  auto stage_of = [&](auto u) {
+    constexpr int v = decltype(u)::value % S::kStages;
+    if constexpr (v == 0) return stage0;
+    else if constexpr (v == 1) return stage1;
+    else if constexpr (v == 2) return stage2;
+    else return stage3;
+  };
+  auto scale_at = [&](auto u) {
+    constexpr int v = decltype(u)::value % S::kStages;
+    if constexpr (v == 0) return scale0;
+    else if constexpr (v == 1) return scale1;
+    else if constexpr (v == 2) return scale2;
+    else return scale3;
   };
 
+  // fragment addresses in a stage; chunk g + 4 is 64 bytes on or back
   const int wm = wave / S::WN, wn = wave % S::WN;
   const int r = lane & 15, g = lane >> 4;
-  const int frag_at = r * kStageRow + ((g ^ ((r >> 1) & 7)) << 4);   // chunk g of row r; chunk g + 4 is 64 bytes on or back
-  const int x_at = wm * S::TM * 16 * kStageRow + frag_at;
-  const int w_at = (S::BM + wn * S::TN * 16) * kStageRow + frag_at;
-  const int col0 = n0 + wn * S::TN * 16;
-  const int sblk = (col0 < p.n ? col0 : p.n - 1) >> 7;
-  // the scale of this wave's columns, read a block ahead (a vector load: a scalar
-  // one would make every wait for an LDS read of its block a full one)
-  const float *wsp = FP8 ? p.w_scale + ((size_t)expert * fp8::ceil_div(p.n, 128) + uniform(sblk)) * p.nb : nullptr;
-  auto scale_of = [&](int b) { return FP8 ? wsp[b < p.nb ? b : p.nb - 1] : 0.0f; };
+  const int x_at = (wm * S::TM * 16 + r) * kStageRow + ((g ^ (r >> 1 & 7)) << 4);
+  const int w_row = S::kPairs ? (r >> 2) * 8 + (r & 3) : r;
+  const int w_f = S::kPairs ? (r >> 1 & 1) | (r >> 2) << 1 : r >> 1 & 7;
+  const int w_at = (S::BM + wn * S::TN * 16 + w_row) * kStageRow + ((g ^ w_f) << 4);
+  auto w_tile = [](int j) { return S::kPairs ? (j >> 1) * 32 * kStageRow + (j & 1) * 4 * kStageRow : j * 16 * kStageRow; };
 
-  v4f acc[S::TM][S::TN];
-#pragma unroll
-  for (int i = 0; i < S::TM; ++i)
-#pragma unroll
-    for (int j = 0; j < S::TN; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+  Tile t = locate(first + at);
+  Loads loads = loads_of(t);
+  issue_first(loads, t);
+  for (;;) {
+    const int col0 = t.n0 + wn * S::TN * 16;
+    // the scale of this wave's columns, read a block ahead (a vector load: a scalar
+    // one would make every wait for an LDS read of its block a full one)
+    const float *wsp = nullptr;
+    if constexpr (FP8)
+      wsp = p.w_scale + ((size_t)t.expert * fp8::ceil_div(p.n, 128) + ((col0 < p.n ? col0 : p.n - 1) >> 7)) * p.nb;
+    auto scale_of = [&](int b) { return FP8 ? wsp[b < p.nb ? b : p.nb - 1] : 0.0f; };
 
-  // One block: the wave's weight operands stay in registers, the rows of x pass
-  // one 16-row tile after the other, and a tile's products are added one tile
-  // later, so that the fma run beside the matrix instructions. The last tile of
-  // a block is multiplied after the barrier, each weight operand making room for
-  // the next block's as it is used: the matrix cores have work while the first
-  // reads of a stage are under way. With next_too the loads of the next block (a
-  // whole one) go out over the first half.
-  Operand<KIND> wf[S::TN], xf[2];   // xf[1] between blocks: the last tile of the block before
-  v4f d[2][S::TN];                  // d[0] between blocks: the products of the tile before that
-  float s[2] = {0.0f, 0.0f};        // scales of the tiles in xf[1] and d[0]: s[1], s[0]
-  float ws_before = 0.0f;
-  static_assert(S::TM % 2 == 0, "tiles alternate between two registers");
-  {
-    const Frag none = {{0, 0, 0, 0}, {0, 0, 0, 0}};
-    xf[1].set(none);
-#pragma unroll
-    for (int j = 0; j < S::TN; ++j) {
-      wf[j].set(none);
-      d[0][j] = kZero4;
-    }
-  }
-  auto compute = [&](auto next_too, int b, float ws, const uint8_t *stage, const float *scale, uint8_t *next, float *next_scale) {
-    constexpr int kEvery = (S::kLoads + (S::TM + 1) / 2 - 1) / ((S::TM + 1) / 2);
-    auto read = [&](int lo, int hi, int rows16, Operand<KIND> &to) {
-      Frag f;
-      f.lo = *reinterpret_cast<const v4i *>(stage + lo + rows16 * 2048);
-      f.hi = *reinterpret_cast<const v4i *>(stage + hi + rows16 * 2048);
-      to.set(f);
-    };
-#pragma unroll
-    for (int i = -1; i < S::TM - 1; ++i) {
-      // i = -1: the last tile of the block before
-      constexpr int kLast = S::TM - 1;
-      const int now = i & 1, then = now ^ 1;                 // buffers of this tile and of its neighbours
-      const int tile = i < 0 ? kLast : i, back = i < 0 ? kLast - 1 : i == 0 ? kLast : i - 1;
-      const float before = s[then] * (i <= 0 ? ws_before : ws);
-      if constexpr (FP8) s[then] = scale[(wm * S::TM + i + 1) * 16 + r];
-      read(x_at, x_at ^ 64, i + 1, xf[then]);
-      if constexpr (decltype(next_too)::value) {
-        if (i < 0) load_scales(b + 1, next_scale);
-#pragma unroll
-        for (int l = (i + 1) * kEvery; l < (i + 2) * kEvery && l < S::kLoads; ++l) load_piece(l, b + 1, next, false);
-      }
+    // The wave's weight operands stay in registers, the rows of x pass one
+    // 16-row tile after the other, and a tile's products are added one tile
+    // later, so that the fma run beside the matrix instructions. The last tile
+    // of a block is multiplied after the barrier, each weight operand making
+    // room for the next block's as it is used: the matrix cores have work while
+    // the first reads of a stage are under way.
+    v4f acc[S::TM][S::TN];
+    Operand<KIND> wf[S::TN], xf[2];   // xf[1] between blocks: the last tile of the block before
+    v4f d[2][S::TN];                  // d[0] between blocks: the products of the tile before that
+    float s[2] = {0.0f, 0.0f};        // scales of the tiles in xf[1] and d[0]: s[1], s[0]
+    float ws_before = 0.0f;
+    {
+      const Frag none = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+      xf[1].set(none);
 #pragma unroll
       for (int j = 0; j < S::TN; ++j) {
-        if constexpr (FP8) {
-          d[now][j] = mma_block<KIND>(wf[j], xf[now], kZero4);
-          scaled_add(before, d[then][j], acc[back][j]);
-        } else {
-          acc[tile][j] = mma_block<KIND>(wf[j], xf[now], acc[tile][j]);
-        }
-        if (i < 0) read(w_at, w_at ^ 64, j, wf[j]);
-        // keeps the fma of a result TN matrix instructions behind it
-        if (KIND == kNative) __builtin_amdgcn_sched_barrier(0);
+        wf[j].set(none);
+        d[0][j] = kZero4;
+#pragma unroll
+        for (int i = 0; i < S::TM; ++i) acc[i][j] = kZero4;
       }
-      __builtin_amdgcn_sched_barrier(0);
     }
-    ws_before = ws;
-  };
-
-  issue(blk0, stage0, scale0);
-  int b = blk0;
-  float ws = scale_of(b);
-  for (; b + 3 < blk1; b += 2) {   // the loads sent here are all of whole blocks
-    stage_barrier();
-    const float ws1 = scale_of(b + 1);
-    compute(std::true_type{}, b, ws, stage0, scale0, stage1, scale1);
-    stage_barrier();
-    ws = scale_of(b + 2);
-    compute(std::true_type{}, b + 1, ws1, stage1, scale1, stage0, scale0);
-  }
-  const int left = blk1 - b;       // one to three blocks, the first of them on its way
-  const float ws1 = scale_of(b + 1), ws2 = scale_of(b + 2);
-  stage_barrier();
-  if (left > 1) issue(b + 1, stage1, scale1);
-  compute(std::false_type{}, b, ws, stage0, scale0, nullptr, nullptr);
-  if (left > 1) {
-    stage_barrier();
-    if (left > 2) issue(b + 2, stage0, scale0);
-    compute(std::false_type{}, b + 1, ws1, stage1, scale1, nullptr, nullptr);
-    if (left > 2) {
-      stage_barrier();
-      compute(std::false_type{}, b + 2, ws2, stage0, scale0, nullptr, nullptr);
-    }
-  }
-
-  // the last tile of the last block
+    // One block. With next_too the loads of block `sent` (a whole one) go out
+    // over the first half.
+    auto compute = [&](auto next_too, int sent, float ws, const uint8_t *stage, const float *scale, uint8_t *next,
+                       float *next_scale) {
+      constexpr int kEvery = (S::kLoads + (S::TM + 1) / 2 - 1) / ((S::TM + 1) / 2);
+      auto read = [&](int lo, int more, Operand<KIND> &to) {
+        Frag f;
+        f.lo = *reinterpret_cast<const v4i *>(stage + lo + more);
+        f.hi = *reinterpret_cast<const v4i *>(stage + (lo ^ 64) + more);
+        to.set(f);
+      };
 #pragma unroll
-  for (int j = 0; j < S::TN; ++j) {
-    if constexpr (FP8) {
-      scaled_add(s[0] * ws_before, d[0][j], acc[S::TM - 2][j]);
-      scaled_add(s[1] * ws_before, mma_block<KIND>(wf[j], xf[1], kZero4), acc[S::TM - 1][j]);
-    } else {
-      acc[S::TM - 1][j] = mma_block<KIND>(wf[j], xf[1], acc[S::TM - 1][j]);
-    }
-  }
-
-  // lane: columns 4 g .. 4 g + 3 of row r of each 16 x 16 tile
+      for (int i = -1; i < S::TM - 1; ++i) {
+        // i = -1: the last tile of the block before
+        constexpr int kLast = S::TM - 1;
+        const int now = i & 1, then = now ^ 1;                 // buffers of this tile and of its neighbours
+        const int tile = i < 0 ? kLast : i, back = i < 0 ? kLast - 1 : i == 0 ? kLast : i - 1;
+        const float before = s[then] * (i <= 0 ? ws_before : ws);
+        if constexpr (FP8) s[then] = scale[(wm * S::TM + i + 1) * 16 + r];
+        read(x_at, (i + 1) * 16 * kStageRow, xf[then]);
+        if constexpr (decltype(next_too)::value) {
+          if (i < 0) load_scales(loads, sent, next_scale);
 #pragma unroll
-  for (int i = 0; i < S::TM; ++i) {
-    const int row = m0 + (wm * S::TM + i) * 16 + r;
-    if (row >= end) continue;
-    bool ok = true;
-    if constexpr (GROUPED) {
-      int src;
-      ok = source_row(p, row, src);
+          for (int l = (i + 1) * kEvery; l < (i + 2) * kEvery && l < S::kLoads; ++l) load_piece(loads, l, sent, next, false);
+        }
+#pragma unroll
+        for (int j = 0; j < S::TN; ++j) {
+          if constexpr (FP8) {
+            d[now][j] = mma_block<KIND>(wf[j], xf[now], kZero4);
+            scaled_add(before, d[then][j], acc[back][j]);
+          } else {
+            acc[tile][j] = mma_block<KIND>(wf[j], xf[now], acc[tile][j]);
+          }
+          if (i < 0) read(w_at, w_tile(j), wf[j]);
+          // keeps the fma of a result TN matrix instructions behind it
+          if (KIND == kNative) __builtin_amdgcn_sched_barrier(0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      ws_before = ws;
+    };
+
+    int b = t.blk0;
+    float ws = scale_of(b);
+    // one step of the steady loop: block b + u, sending b + u + kAhead (a whole one)
+    auto step = [&](auto u) {
+      constexpr int v = decltype(u)::value;
+      using Next = std::integral_constant<int, v + kAhead>;
+      stage_barrier<kAfter>();
+      const float ws_next = scale_of(b + v + 1);
+      compute(std::true_type{}, b + v + kAhead, ws, stage_of(u), scale_at(u), stage_of(Next{}), scale_at(Next{}));
+      ws = ws_next;
+    };
+    // one of the last blocks: block b + u of `left`, sending b + u + kAhead if there is one
+    auto last_step = [&](auto u, int left) {
+      constexpr int v = decltype(u)::value;
+      using Next = std::integral_constant<int, v + kAhead>;
+      if (v >= left) return;
+      stage_barrier<0>();
+      const float ws_next = scale_of(b + v + 1);
+      if (v + kAhead < left) issue(loads, b + v + kAhead, stage_of(Next{}), scale_at(Next{}));
+      compute(std::false_type{}, 0, ws, stage_of(u), scale_at(u), nullptr, nullptr);
+      ws = ws_next;
+    };
+    using U0 = std::integral_constant<int, 0>;
+    using U1 = std::integral_constant<int, 1>;
+    using U2 = std::integral_constant<int, 2>;
+    using U3 = std::integral_constant<int, 3>;
+    using U4 = std::integral_constant<int, 4>;
+    using U5 = std::integral_constant<int, 5>;
+    using U6 = std::integral_constant<int, 6>;
+    for (; b + 2 * S::kStages - 1 < t.blk1; b += S::kStages) {
+      step(U0{});
+      step(U1{});
+      if constexpr (S::kStages > 2) step(U2{});
+      if constexpr (S::kStages > 3) step(U3{});
     }
+    const int left = t.blk1 - b;   // 1 to 2 kStages - 1
+    last_step(U0{}, left);
+    last_step(U1{}, left);
+    last_step(U2{}, left);
+    if constexpr (S::kStages > 2) {
+      last_step(U3{}, left);
+      last_step(U4{}, left);
+    }
+    if constexpr (S::kStages > 3) {
+      last_step(U5{}, left);
+      last_step(U6{}, left);
+    }
+
+    // all waves are through with the stages: the next tile's loads may go
+    at += stride;
+    const bool more = at < count;
+    const Tile done = t;
+    stage_barrier<63>();
+    if (more) {
+      t = locate(first + at);
+      loads = loads_of(t);
+      issue_first(loads, t);
+    }
+
+    // the last tile of the last block
 #pragma unroll
     for (int j = 0; j < S::TN; ++j) {
-      const int col = col0 + j * 16 + g * 4;
-      const v4f zero = {0.0f, 0.0f, 0.0f, 0.0f};
-      const v4f v = ok ? acc[i][j] : zero;
-      if (!GROUPED && p.splits > 1) {
-        float *to = p.part + ((size_t)part * p.rows + row) * p.n + col;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (col + e < p.n) to[e] = v[e];
-        continue;
-      }
-      if ((p.n & 3) == 0) {   // four columns at once: rows of y keep the alignment of y
-        if (col >= p.n) continue;
-        const size_t at = (size_t)row * p.n + col;
-        if (p.y_bf16) {
-          typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-          *reinterpret_cast<bf16x4 *>(static_cast<__bf16 *>(p.y) + at) =
-              bf16x4{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]};
-        } else {
-          *reinterpret_cast<v4f *>(static_cast<float *>(p.y) + at) = v;
-        }
+      if constexpr (FP8) {
+        scaled_add(s[0] * ws_before, d[0][j], acc[S::TM - 2][j]);
+        scaled_add(s[1] * ws_before, mma_block<KIND>(wf[j], xf[1], kZero4), acc[S::TM - 1][j]);
       } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (col + e < p.n) store_y(p, row, col + e, v[e]);
+        acc[S::TM - 1][j] = mma_block<KIND>(wf[j], xf[1], acc[S::TM - 1][j]);
       }
     }
+
+    // A lane holds, of row r of each 16 rows of x, columns 8 g .. 8 g + 7 of each
+    // 32 (from two tiles), or 4 g .. 4 g + 3 of each 16.
+    constexpr int kWide = S::kPairs ? 8 : 4;
+    const bool part = !GROUPED && p.splits > 1, bf16 = p.y_bf16 && !part;
+    const bool whole = p.n % (bf16 ? kWide : 4) == 0;   // then rows of y keep the alignment that the stores need
+    uint8_t *to = part ? reinterpret_cast<uint8_t *>(p.part + (size_t)done.part * p.rows * p.n) : static_cast<uint8_t *>(p.y);
+#pragma unroll
+    for (int i = 0; i < S::TM; ++i) {
+      const int row = done.m0 + (wm * S::TM + i) * 16 + r;
+      if (row >= done.end) continue;
+#pragma unroll
+      for (int j = 0; j < S::TN; j += S::kPairs ? 2 : 1) {
+        const int col = col0 + j * 16 + g * kWide;
+        float v[kWide];
+#pragma unroll
+        for (int e = 0; e < kWide; ++e) v[e] = acc[i][j + e / 4][e % 4];
+        const size_t place = (size_t)row * p.n + col;
+        if (!whole) {
+#pragma unroll
+          for (int e = 0; e < kWide; ++e)
+            if (col + e < p.n) {
+              if (bf16)
+                reinterpret_cast<__bf16 *>(to)[place + e] = (__bf16)v[e];
+              else
+                reinterpret_cast<float *>(to)[place + e] = v[e];
+            }
+        } else if (bf16) {
+          if (col >= p.n) continue;
+          typedef __bf16 Row __attribute__((ext_vector_type(kWide)));
+          Row o;
+#pragma unroll
+          for (int e = 0; e < kWide; ++e) o[e] = (__bf16)v[e];
+          *reinterpret_cast<Row *>(reinterpret_cast<__bf16 *>(to) + place) = o;
+        } else {
+#pragma unroll
+          for (int e = 0; e < kWide; e += 4)
+            if (col + e < p.n)
+              *reinterpret_cast<v4f *>(reinterpret_cast<float *>(to) + place + e) = v4f{v[e], v[e + 1], v[e + 2], v[e + 3]};
+        }
+      }
+    }
+    if (!more) return;
   }
 }
 
@@ -616,28 +724,29 @@ __global__ __launch_bounds__(256) void product_sum_kernel(const float *__restric
     static_cast<float *>(p.y)[at] = v;
 }
 
-using Tile32 = Shape<32, 128, 1, 4>;
-using Tile64 = Shape<64, 128, 1, 4>;
-using Tile128 = Shape<128, 128, 2, 2>;
-using Tile256 = Shape<256, 256, 2, 4>;
+using Tile32 = Shape<32, 64, 1, 4, 4>;
+using Tile64 = Shape<64, 128, 1, 4, 3>;
+using Tile128 = Shape<128, 128, 4, 2, 4>;
+using Tile256 = Shape<256, 128, 4, 2, 3>;
+using Tile256Wide = Shape<256, 256, 2, 4, 2>;
 
 template <class S, Kind KIND, bool GROUPED>
-int launch_tile(const ProductArgs &a, unsigned grid, hipStream_t s) {
-  return launch_kernel("product_tile_kernel", product_tile_kernel<S, KIND, GROUPED>, dim3(grid), dim3(S::kThreads), 0,
-                       s, a);
+int launch_tile(const ProductArgs &a, hipStream_t s) {
+  const int64_t row_tiles = GROUPED ? fp8::grouped_row_tiles(a.rows, a.n_experts, S::BM) : fp8::ceil_div(a.rows, S::BM);
+  const int64_t tiles = row_tiles * fp8::ceil_div(a.n, S::BN) * a.splits, most = (int64_t)S::kPerCu * fp8::kSlots;
+  return launch_kernel("product_tile_kernel", product_tile_kernel<S, KIND, GROUPED>,
+                       dim3((unsigned)(tiles < most ? tiles : most)), dim3(S::kThreads), 0, s, a);
 }
 
 template <Kind KIND, bool GROUPED>
 int launch_tiles(int tile, const ProductArgs &a, hipStream_t s) {
-  const int bm = fp8::tile_rows(tile), bn = fp8::tile_cols(tile);
-  const int64_t row_tiles = GROUPED ? fp8::grouped_row_tiles(a.rows, a.n_experts, bm) : fp8::ceil_div(a.rows, bm);
-  const unsigned grid = (unsigned)(row_tiles * fp8::ceil_div(a.n, bn) * a.splits);
   switch (tile) {
-    case fp8::kTile32: return launch_tile<Tile32, KIND, GROUPED>(a, grid, s);
-    case fp8::kTile64: return launch_tile<Tile64, KIND, GROUPED>(a, grid, s);
-    case fp8::kTile128: return launch_tile<Tile128, KIND, GROUPED>(a, grid, s);
+    case fp8::kTile32: return launch_tile<Tile32, KIND, GROUPED>(a, s);
+    case fp8::kTile64: return launch_tile<Tile64, KIND, GROUPED>(a, s);
+    case fp8::kTile128: return launch_tile<Tile128, KIND, GROUPED>(a, s);
+    case fp8::kTile256: return launch_tile<Tile256, KIND, GROUPED>(a, s);
     default:
-      if constexpr (KIND == kNative && !GROUPED) return launch_tile<Tile256, KIND, GROUPED>(a, grid, s);
+      if constexpr (KIND != kExact) return launch_tile<Tile256Wide, KIND, GROUPED>(a, s);
       set_error_detail("product_tile_kernel", 0, "no such tile");
       return QMV_ERR_HIP;
   }
@@ -670,14 +779,14 @@ int launch_fp8_dense(const ProductArgs &a, void *stream) {
 
 int launch_fp8_grouped(const ProductArgs &a, void *stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const fp8::GroupedPlan plan = fp8::grouped_plan(a.rows, a.n_experts);
+  const fp8::GroupedPlan plan = fp8::grouped_plan(a.rows, a.n_experts, !a.y_bf16);
   if (plan.stream) return launch_stream<kExact, true>(a, s);
   return a.y_bf16 ? launch_tiles<kNative, true>(plan.tile, a, s) : launch_tiles<kExact, true>(plan.tile, a, s);
 }
 
 int launch_bf16_grouped(const ProductArgs &a, void *stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const fp8::GroupedPlan plan = fp8::grouped_plan(a.rows, a.n_experts);
+  const fp8::GroupedPlan plan = fp8::grouped_plan(a.rows, a.n_experts, false);
   return plan.stream ? launch_stream<kBf16, true>(a, s) : launch_tiles<kBf16, true>(plan.tile, a, s);
 }
 
