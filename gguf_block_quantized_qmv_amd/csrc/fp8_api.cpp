@@ -59,7 +59,7 @@ int grouped(const void *w, size_t w_bytes, const float *w_scale, const void *x, 
   const size_t wb = (size_t)n_experts * n * k * value_bytes;   // <= 2^51
   if (w_bytes != wb) return QMV_ERR_SIZE;
   if (rows == 0) return QMV_OK;
-  if (!qmv::fp8::grouped_fits_grid(rows, n, n_experts, e4m3 && y_type == QMM_F32)) return QMV_ERR_RANGE;
+  if (!qmv::fp8::grouped_in_grid(rows, n, n_experts, e4m3 && y_type == QMM_F32)) return QMV_ERR_RANGE;
   // rows are gathered by 32-bit byte offsets
   if (row_index && (size_t)x_rows * k * value_bytes > UINT32_MAX) return QMV_ERR_RANGE;
   // with no row of x every index is out of range, and x itself may be null
@@ -90,13 +90,11 @@ int grouped(const void *w, size_t w_bytes, const float *w_scale, const void *x, 
   a.nb = qmv::fp8::blocks_of(a.k_bytes);
   a.n_experts = n_experts;
   a.y_bf16 = y_type == QMM_BF16;
-  a.splits = 1;
   return e4m3 ? qmv::launch_fp8_grouped(a, stream) : qmv::launch_bf16_grouped(a, stream);
 }
 
-bool dense_in_range(int m, int n, int k, int y_type) {
-  return m >= 1 && m <= QMM_MAX_ROWS && check_nk(n, k, 16) == QMV_OK && 
-         qmv::fp8::dense_fits_grid(m, n, k, y_type == QMM_BF16);
+bool dense_in_range(int m, int n, int k) {
+  return m >= 1 && m <= QMM_MAX_ROWS && check_nk(n, k, 16) == QMV_OK && qmv::fp8::dense_in_grid(m, n);
 }
 
 }  // namespace
@@ -112,7 +110,7 @@ int qmm_fp8_quant_silu_mul(const void *x, int x_type, uint8_t *xq, float *xs, in
 }
 
 size_t qmm_fp8_workspace(int m, int n, int k, int y_type) {
-  if (!type_ok(y_type) || !dense_in_range(m, n, k, y_type)) return 0;
+  if (!type_ok(y_type) || !dense_in_range(m, n, k)) return 0;
   return qmv::fp8::dense_workspace(m, n, k, y_type == QMM_BF16);
 }
 
@@ -123,7 +121,7 @@ int qmm_fp8(const void *w, size_t w_bytes, const float *w_scale, const void *x, 
   if (m < 1 || m > QMM_MAX_ROWS) return QMV_ERR_RANGE;
   const int rc = check_nk(n, k, 16);
   if (rc) return rc;
-  if (!dense_in_range(m, n, k, y_type)) return QMV_ERR_RANGE;
+  if (!dense_in_range(m, n, k)) return QMV_ERR_RANGE;
   const size_t wb = (size_t)n * k;
   if (w_bytes != wb) return QMV_ERR_SIZE;
   if (!aligned(w, 16) || !aligned(x, 16) || !aligned(y, 16) || !aligned(w_scale, 4) || !aligned(x_scale, 4) ||
@@ -155,7 +153,6 @@ int qmm_fp8(const void *w, size_t w_bytes, const float *w_scale, const void *x, 
   a.nb = qmv::fp8::blocks_of(k);
   a.n_experts = 1;
   a.y_bf16 = y_type == QMM_BF16;
-  a.splits = qmv::fp8::dense_plan(m, n, k, y_type == QMM_BF16).splits;
   return qmv::launch_fp8_dense(a, stream);
 }
 

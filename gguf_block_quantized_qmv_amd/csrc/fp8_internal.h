@@ -18,8 +18,8 @@ struct ProductArgs {
   const int32_t *offsets;  // null: dense
   const int32_t *index;    // null: row r of x
   void *y;
-  float *part;             // dense with splits > 1
-  int rows, x_rows, n, k_bytes, nb, n_experts, y_bf16, splits;
+  float *part;             // the workspace of a dense plan with parts
+  int rows, x_rows, n, k_bytes, nb, n_experts, y_bf16;
 };
 
 int launch_fp8_quant(const void *x, bool x_f32, bool gated, uint8_t *xq, float *xs, int m, int k, void *stream);

@@ -29,26 +29,80 @@ constexpr int tile_cols(int t) { return t == kTile32 ? 64 : t == kTile256Wide ? 
 
 // ---- dense -------------------------------------------------------------------
 
+// A few rows of x against a matrix that is soon read: `stream`, the kernel that
+// takes the weights straight into registers, every wave a share of k. Else
+// tiles: t_main whole ones (a multiple of the CUs, or all), and r_tiles that
+// are cut into `splits` parts of k so that the last round fills the CUs; the
+// parts' fp32 sums go to the workspace and a second launch adds them in order.
 struct DensePlan {
-  bool stream;   // the weight-streaming kernel (m <= QMM_SAME_ROWS), no workspace
-  int tile;      // else a Tile
-  int splits;    // parts of k, summed by a second launch when more than one
+  bool stream;
+  int tile, t_main, r_tiles, splits;
 };
 
-// The weight-streaming kernel: `tile` weight rows (a multiple of four, so that
-// a lane's four results lie under one scale) and `waves` waves a workgroup.
-// The tile is the one of 16, 12 and 8 rows that spreads the workgroups most
-// evenly over the CUs; with few rows, shorter tiles keep every CU at work.
-// About sixteen waves a CU keep the memory busy.
+// The streaming kernel reads the weights once per 16 rows of x, from the L2
+// after the first; up to here that is quicker than tiles and their parts
+// (1 x 4096 x 4096: 8 us against 15; 1 x 17408 x 5120: 26 against 20).
+constexpr int64_t kStreamBytes = (int64_t)32 << 20;
+
+inline DensePlan split_plan(int tile, int m, int n, int nb) {
+  DensePlan p{false, tile, 0, 0, 1};
+  const int64_t tiles = (int64_t)ceil_div(m, tile_rows(tile)) * ceil_div(n, tile_cols(tile));
+  // small tiles share a CU: a second round of them costs little
+  const int64_t rest = tile <= kTile64 && tiles >= kSlots ? 0 : tiles % kSlots;
+  int64_t s = rest ? kSlots / rest : 1;
+  if (s > nb / 4) s = nb / 4;      // at least four blocks a part
+  if (s > 16) s = 16;
+  p.splits = s < 1 ? 1 : (int)s;
+  p.r_tiles = p.splits > 1 ? (int)rest : 0;
+  p.t_main = (int)(tiles < INT32_MAX ? tiles : INT32_MAX) - p.r_tiles;
+  return p;
+}
+
+inline size_t split_bytes(const DensePlan &p) {
+  return p.splits > 1 ? (size_t)p.r_tiles * p.splits * tile_rows(p.tile) * tile_cols(p.tile) * 4 : 0;
+}
+
+inline DensePlan dense_plan(int m, int n, int k, bool y_bf16) {
+  const int nb = blocks_of(k);
+  if ((int64_t)n * k * ceil_div(m, 16) < kStreamBytes) return DensePlan{true, kTile32, 0, 0, 1};
+  if (m <= 128) return split_plan(m <= 32 ? kTile32 : m <= 64 ? kTile64 : kTile128, m <= 32 ? 32 : m, n, nb);
+  // Of the large tiles the one with the least time by this model, in ns: a step
+  // of one block of k takes, with every CU at work, 1800 (256 x 256), 1150
+  // (256 x 128) and 750 (128 x 128), in fp32 results 2200 and 1300; a tile
+  // starts and ends in 8000; parts are written and read at 5 bytes a ps.
+  DensePlan best{};
+  int64_t least = INT64_MAX;
+  for (int tile = kTile128; tile <= (y_bf16 ? kTile256Wide : kTile256); ++tile) {
+    const DensePlan p = split_plan(tile, m, n, nb);
+    const int64_t step = tile == kTile256Wide ? 1800 : tile == kTile256 ? (y_bf16 ? 1150 : 2200) : y_bf16 ? 750 : 1300;
+    const int64_t rounds = (p.t_main + kSlots - 1) / kSlots;
+    int64_t cost = rounds * (nb * step + 8000);
+    if (p.r_tiles) cost += ceil_div(nb, p.splits) * step + 8000 + 3000 + (int64_t)split_bytes(p) * 2 / 5000;
+    if (cost < least) {
+      least = cost;
+      best = p;
+    }
+  }
+  return best;
+}
+
+inline size_t dense_workspace(int m, int n, int k, bool y_bf16) { return split_bytes(dense_plan(m, n, k, y_bf16)); }
+
+// The streaming kernel: `tile` weight rows (a multiple of four, so that a
+// lane's four results lie under one scale) and `waves` waves a workgroup, one
+// for each 16 rows of x. The tile is the one of 16, 12 and 8 rows that spreads
+// the workgroups most evenly over the CUs; with few rows, shorter tiles keep
+// every CU at work.
 struct StreamPlan {
   int tile, waves;
 };
 
-inline StreamPlan stream_plan(int n, int nb, int slots) {
+inline StreamPlan stream_plan(int m, int n, int nb) {
+  const int chunks = ceil_div(m, 16);   // one for every m that shares its bits
   int tile = 4;
   int64_t best_num = 0, best_den = 1, per_cu = 1;
   for (int t = 16; t >= 8; t -= 4) {
-    const int64_t groups = (int64_t)ceil_div(n, t) * slots, rounds = (groups + kSlots - 1) / kSlots;
+    const int64_t groups = (int64_t)ceil_div(n, t) * chunks, rounds = (groups + kSlots - 1) / kSlots;
     if (groups * best_den > best_num * rounds * kSlots) {   // share of the CUs' rounds that has work
       best_num = groups;
       best_den = rounds * kSlots;
@@ -62,52 +116,12 @@ inline StreamPlan stream_plan(int n, int nb, int slots) {
   return StreamPlan{tile, waves};
 }
 
-inline DensePlan dense_plan(int m, int n, int k, bool y_bf16) {
-  DensePlan p{false, kTile128, 1};
-  const int nb = blocks_of(k);
-  if (m <= 32) {
-    // by (n, k) alone
-    p.tile = kTile32;
-    p.stream = (int64_t)n * k < (int64_t)32 << 20;
-    if (p.stream) return p;
-  } else {
-    p.tile = m <= 64 ? kTile64 : m <= 128 ? kTile128 : kTile256;
-    const int64_t wide = (int64_t)ceil_div(m, 256) * ceil_div(n, 256);
-    if (y_bf16 && m > 128 && wide >= kSlots) p.tile = kTile256Wide;
-  }
-  const int64_t tiles = (int64_t)(m <= 32 ? 1 : ceil_div(m, tile_rows(p.tile))) * ceil_div(n, tile_cols(p.tile));
-  int64_t s = kSlots / tiles;
-  if (s > nb / 4) s = nb / 4;      // at least four blocks a part
-  if (s > 16) s = 16;
-  p.splits = s < 1 ? 1 : (int)s;
-  return p;
-}
-
-inline size_t dense_workspace(int m, int n, int k, bool y_bf16) {
-  const DensePlan p = dense_plan(m, n, k, y_bf16);
-  return p.splits > 1 ? (size_t)p.splits * (size_t)m * (size_t)n * 4 : 0;
-}
-
 // ---- grouped -----------------------------------------------------------------
 
-// Expected rows of an expert that has any: host code cannot see the offsets, so
-// the tile goes by rows spread evenly.
-struct GroupedPlan {
-  bool stream;
-  int tile;
-};
-
-inline GroupedPlan grouped_plan(int rows, int n_experts, bool exact) {
+// Host code cannot see the offsets: the tile goes by the rows spread evenly.
+inline int grouped_tile(int rows, int n_experts, bool exact) {
   const int avg = rows / (n_experts < 1 ? 1 : n_experts);
-#ifndef GSTREAM
-#define GSTREAM 0
-#endif
-#ifndef GBIG
-#define GBIG kTile256
-#endif
-  GroupedPlan p{rows <= GSTREAM, kTile32};
-  p.tile = avg <= 24 ? kTile32 : avg <= 64 ? kTile64 : avg <= 128 ? kTile128 : exact ? kTile256 : GBIG;
-  return p;
+  return avg <= 24 ? kTile32 : avg <= 64 ? kTile64 : avg <= 128 ? kTile128 : exact ? kTile256 : kTile256Wide;
 }
 
 // Row tiles a grouped launch can need: every expert with rows may have one
@@ -116,17 +130,14 @@ inline int64_t grouped_row_tiles(int rows, int n_experts, int bm) {
   return (int64_t)rows / bm + (rows < n_experts ? rows : n_experts);
 }
 
-// Workgroups of a launch: 2^22 of up to 512 threads keep a grid inside 32 bits.
-constexpr int64_t kMaxWorkgroups = (int64_t)1 << 22;
+// Tiles of a launch stay far inside 32 bits.
+constexpr int64_t kMaxTiles = (int64_t)1 << 28;
 
-inline bool dense_fits_grid(int m, int n, int k, bool y_bf16) {
-  const DensePlan p = dense_plan(m, n, k, y_bf16);
-  return p.stream || (int64_t)ceil_div(m, tile_rows(p.tile)) * ceil_div(n, tile_cols(p.tile)) * p.splits <= kMaxWorkgroups;
-}
+inline bool dense_in_grid(int m, int n) { return (int64_t)ceil_div(m, 128) * ceil_div(n, 64) <= kMaxTiles; }
 
-inline bool grouped_fits_grid(int rows, int n, int n_experts, bool exact) {
-  const GroupedPlan p = grouped_plan(rows, n_experts, exact);
-  return p.stream || grouped_row_tiles(rows, n_experts, tile_rows(p.tile)) * ceil_div(n, tile_cols(p.tile)) <= kMaxWorkgroups;
+inline bool grouped_in_grid(int rows, int n, int n_experts, bool exact) {
+  const int t = grouped_tile(rows, n_experts, exact);
+  return grouped_row_tiles(rows, n_experts, tile_rows(t)) * ceil_div(n, tile_cols(t)) <= kMaxTiles;
 }
 
 }  // namespace fp8

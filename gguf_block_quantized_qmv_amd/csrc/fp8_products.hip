@@ -114,151 +114,107 @@ __device__ __forceinline__ void expert_rows(const int32_t *__restrict__ offsets,
   end = clampi(offsets[e + 1], begin, rows);
 }
 
-// Row of x behind row `row` of y; false (and row 0) for an index outside x.
-__device__ __forceinline__ bool source_row(const ProductArgs &p, int row, int &src) {
-  src = p.index ? p.index[row] : row;
-  const bool ok = (unsigned)src < (unsigned)p.x_rows;
-  src = ok ? src : 0;
-  return ok;
-}
-
-__device__ __forceinline__ void store_y(const ProductArgs &p, int row, int col, float v) {
-  const size_t at = (size_t)row * p.n + col;
-  if (p.y_bf16)
-    static_cast<__bf16 *>(p.y)[at] = (__bf16)v;
-  else
-    static_cast<float *>(p.y)[at] = v;
-}
-
 // ---- a few rows: stream the weights ---------------------------------------------
 //
-// A workgroup owns `tile` <= 16 rows of one weight matrix and up to 16 rows of
-// x at a time; wave v takes blocks v, v + NW, ... of k straight from memory
-// into MFMA fragments (no LDS), kDepth blocks in flight, and the waves' sums
-// are added in wave order. Bound by the weight stream. The host chooses the
-// tile so that every CU gets the same number of workgroups (a tile shorter
-// than 16 rows repeats its last row: matrix work, no memory traffic). The order
-// of the sums goes by (n, k) alone and the columns of an MFMA do not mix, so a
-// row of x has the same bits in any company. Grouped: workgroup (t, s) serves
-// the s-th expert that has rows, and takes 16 of its rows at a time.
+// A workgroup owns `tile` <= 16 rows of w and 16 rows of x; wave v takes blocks
+// v, v + NW, ... of k straight from memory into MFMA fragments (no LDS), kDepth
+// blocks in flight, and the waves' sums are added in wave order: no second
+// launch. The host chooses the tile so that every CU gets the same number of
+// workgroups (a tile shorter than 16 rows repeats its last row: matrix work, no
+// memory traffic). The order of the sums goes by (n, k) alone and the columns
+// of an MFMA do not mix, so a row of x has the same bits in any company. Bound
+// by the latency of a few rounds of loads and, from some megabytes of weights
+// on, by what a CU takes from the L2 (w and x alike: a tile of 16 rows reads as
+// many bytes of x as of w).
 constexpr int kDepth = 3;
 
-template <Kind KIND, bool GROUPED, int NW>
-__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) void product_stream_kernel(
+template <int NW>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) void fp8_stream_kernel(
     const ProductArgs p, const int tile) {
-  constexpr bool FP8 = is_e4m3(KIND);
   __shared__ float red[NW][256];
   const int lane = (int)threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int n0 = (int)blockIdx.x * tile;
-  const int n1 = n0 + tile < p.n ? n0 + tile : p.n;
-  int expert = 0, begin = 0, end = p.rows;
-  if constexpr (GROUPED) {
-    int want = (int)blockIdx.y, found = -1;
-    for (int base = 0; base < p.n_experts && found < 0; base += 64) {
-      int b0 = 0, b1 = 0;
-      if (base + lane < p.n_experts) expert_rows(p.offsets, base + lane, p.rows, b0, b1);
-      uint64_t mask = __ballot(b1 > b0);
-      const int have = __popcll(mask);
-      if (want < have) {
-        for (int i = 0; i < want; ++i) mask &= mask - 1;
-        found = base + __ffsll((unsigned long long)mask) - 1;
-      }
-      want -= have;
-    }
-    if (found < 0) return;
-    expert = uniform(found);
-    expert_rows(p.offsets, expert, p.rows, begin, end);
-  }
+  const int n0 = (int)blockIdx.x * tile, n1 = n0 + tile < p.n ? n0 + tile : p.n;
+  const int m0 = (int)blockIdx.y * 16, m1 = m0 + 16 < p.rows ? m0 + 16 : p.rows;
   // Lane offsets from scalar addresses. They are hidden from the optimiser at
   // every use, which would otherwise keep one 64-bit address per block alive.
-  const uint8_t *wbase = p.w + ((size_t)expert * p.n + n0) * p.k_bytes;
+  const uint8_t *wbase = p.w + (size_t)n0 * p.k_bytes, *xbase = p.x + (size_t)m0 * p.k_bytes;
   uint32_t wlane = (uint32_t)(n0 + r < n1 ? r : n1 - 1 - n0) * (uint32_t)p.k_bytes + g * 16;
+  uint32_t xlane = (uint32_t)(m0 + r < m1 ? r : m1 - 1 - m0) * (uint32_t)p.k_bytes + g * 16;
   // tiles are multiples of four rows: a lane's four results share a scale
-  const float *wsbase = FP8 ? p.w_scale + (size_t)expert * fp8::ceil_div(p.n, 128) * p.nb : nullptr;
   const int srow = n0 + g * 4 < p.n ? n0 + g * 4 : p.n - 1;
-  uint32_t wslane = FP8 ? (uint32_t)(srow >> 7) * (uint32_t)p.nb : 0;
+  uint32_t wslane = (uint32_t)(srow >> 7) * (uint32_t)p.nb;
+  uint32_t xslane = (uint32_t)(m0 + r < m1 ? m0 + r : m1 - 1);
   const int whole = p.k_bytes >> 7, tail = p.k_bytes & 127;
 
-  for (int t0 = begin; t0 < end; t0 += 16) {
-    int src;
-    const bool in_x = source_row(p, t0 + r < end ? t0 + r : end - 1, src);   // else a row of zeros
-    using Offset = std::conditional_t<GROUPED, uint64_t, uint32_t>;   // dense: within 16 rows
-    Offset xlane = (Offset)src * (Offset)p.k_bytes + (Offset)(g * 16);
-    uint32_t xslane = (uint32_t)src;
-
-    Frag wf[kDepth], xf[kDepth];
-    float xs[kDepth], ws[kDepth];
-    // Block b (past the last whole one: zeros, so that every pass of the loop
-    // sends the same loads and each wait counts exactly those behind it).
-    auto load_scales = [&](int b, int u, bool ok) {
-      if constexpr (FP8) {
-        asm("" : "+v"(xslane), "+v"(wslane));
-        const float *zeros = reinterpret_cast<const float *>(g_zeros);
-        const float *x = (ok ? p.x_scale + (size_t)b * p.x_rows : zeros) + (ok ? xslane : 0);
-        if (GROUPED) x = in_x ? x : zeros;
-        xs[u] = *x;
-        ws[u] = (ok ? wsbase + b : zeros)[ok ? wslane : 0];
-      }
-    };
-    auto load = [&](int b, int u) {
-      asm("" : "+v"(wlane), "+v"(xlane));
-      const bool ok = b < whole;
-      const uint8_t *zeros = reinterpret_cast<const uint8_t *>(g_zeros);
-      const uint8_t *w = (ok ? wbase + (size_t)b * 128 : zeros) + (ok ? wlane : 0);
-      const uint8_t *x = (ok ? p.x + (size_t)b * 128 : zeros) + (ok ? xlane : 0);
-      if (GROUPED) x = in_x ? x : zeros;
-      wf[u].lo = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(w));
-      wf[u].hi = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(w + 64));
-      xf[u].lo = *reinterpret_cast<const v4i *>(x);
-      xf[u].hi = *reinterpret_cast<const v4i *>(x + 64);
-      load_scales(b, u, ok);
-    };
-    v4f acc = kZero4;
-    auto use = [&](int u) {
-      Operand<KIND> a, c;
-      a.set(wf[u]);
-      c.set(xf[u]);
-      if constexpr (FP8)
-        scaled_add(xs[u] * ws[u], mma_block<KIND>(a, c, kZero4), acc);
+  Frag wf[kDepth], xf[kDepth];
+  float xs[kDepth], ws[kDepth];
+  // Block b (past the last whole one: zeros, so that every pass of the loop
+  // sends the same loads and each wait counts exactly those behind it).
+  auto load_scales = [&](int b, int u, bool ok) {
+    asm("" : "+v"(xslane), "+v"(wslane));
+    const float *zeros = reinterpret_cast<const float *>(g_zeros);
+    xs[u] = (ok ? p.x_scale + (size_t)b * p.x_rows : zeros)[ok ? xslane : 0];
+    ws[u] = (ok ? p.w_scale + b : zeros)[ok ? wslane : 0];
+  };
+  auto load = [&](int b, int u) {
+    asm("" : "+v"(wlane), "+v"(xlane));
+    const bool ok = b < whole;
+    const uint8_t *zeros = reinterpret_cast<const uint8_t *>(g_zeros);
+    const uint8_t *w = (ok ? wbase + (size_t)b * 128 : zeros) + (ok ? wlane : 0);
+    const uint8_t *x = (ok ? xbase + (size_t)b * 128 : zeros) + (ok ? xlane : 0);
+    wf[u].lo = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(w));
+    wf[u].hi = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(w + 64));
+    xf[u].lo = *reinterpret_cast<const v4i *>(x);
+    xf[u].hi = *reinterpret_cast<const v4i *>(x + 64);
+    load_scales(b, u, ok);
+  };
+  v4f acc = kZero4;
+  auto use = [&](int u) {
+    Operand<kExact> a, c;
+    a.set(wf[u]);
+    c.set(xf[u]);
+    scaled_add(xs[u] * ws[u], mma_block<kExact>(a, c, kZero4), acc);
+  };
+#pragma unroll
+  for (int u = 0; u < kDepth; ++u) load(wave + u * NW, u);
+  for (int b = wave; b < whole; b += kDepth * NW)
+#pragma unroll
+    for (int u = 0; u < kDepth; ++u) {
+      use(u);
+      load(b + (u + kDepth) * NW, u);
+      __builtin_amdgcn_sched_barrier(0);   // one block's widened operands at a time
+    }
+  if (tail && wave == whole % NW) {   // the partial last block: zeros past the row
+    const v4i none = {0, 0, 0, 0};
+    wf[0].lo = wf[0].hi = xf[0].lo = xf[0].hi = none;
+    const uint8_t *w = wbase + (size_t)whole * 128 + wlane, *x = xbase + (size_t)whole * 128 + xlane;
+    if (g * 16 < tail) {
+      wf[0].lo = *reinterpret_cast<const v4i *>(w);
+      xf[0].lo = *reinterpret_cast<const v4i *>(x);
+    }
+    if (g * 16 + 64 < tail) {
+      wf[0].hi = *reinterpret_cast<const v4i *>(w + 64);
+      xf[0].hi = *reinterpret_cast<const v4i *>(x + 64);
+    }
+    load_scales(whole, 0, true);
+    use(0);
+  }
+  // lane l holds columns 4 g .. 4 g + 3 of row r of x
+  *reinterpret_cast<v4f *>(&red[wave][r * 16 + g * 4]) = acc;
+  __syncthreads();
+  if ((int)threadIdx.x < 256) {
+    const int row = m0 + ((int)threadIdx.x >> 4), col = n0 + ((int)threadIdx.x & 15);
+    float sum = red[0][threadIdx.x];
+#pragma unroll
+    for (int v = 1; v < NW; ++v) sum += red[v][threadIdx.x];
+    if (row < m1 && col < n1) {
+      const size_t at = (size_t)row * p.n + col;
+      if (p.y_bf16)
+        static_cast<__bf16 *>(p.y)[at] = (__bf16)sum;
       else
-        acc = mma_block<KIND>(a, c, acc);
-    };
-#pragma unroll
-    for (int u = 0; u < kDepth; ++u) load(wave + u * NW, u);
-    for (int b = wave; b < whole; b += kDepth * NW)
-#pragma unroll
-      for (int u = 0; u < kDepth; ++u) {
-        use(u);
-        load(b + (u + kDepth) * NW, u);
-        __builtin_amdgcn_sched_barrier(0);   // one block's widened operands at a time
-      }
-    if (tail && wave == whole % NW) {   // the partial last block: zeros past the row
-      const v4i none = {0, 0, 0, 0};
-      wf[0].lo = wf[0].hi = xf[0].lo = xf[0].hi = none;
-      const uint8_t *w = wbase + (size_t)whole * 128 + wlane, *x = p.x + (size_t)whole * 128 + xlane;
-      if (g * 16 < tail) {
-        wf[0].lo = *reinterpret_cast<const v4i *>(w);
-        if (in_x) xf[0].lo = *reinterpret_cast<const v4i *>(x);
-      }
-      if (g * 16 + 64 < tail) {
-        wf[0].hi = *reinterpret_cast<const v4i *>(w + 64);
-        if (in_x) xf[0].hi = *reinterpret_cast<const v4i *>(x + 64);
-      }
-      load_scales(whole, 0, true);
-      use(0);
+        static_cast<float *>(p.y)[at] = sum;
     }
-    // lane l holds columns 4 g .. 4 g + 3 of row r of x
-    *reinterpret_cast<v4f *>(&red[wave][r * 16 + g * 4]) = acc;
-    __syncthreads();
-    if ((int)threadIdx.x < 256) {
-      const int row = t0 + ((int)threadIdx.x >> 4), col = n0 + ((int)threadIdx.x & 15);
-      float sum = red[0][threadIdx.x];
-#pragma unroll
-      for (int v = 1; v < NW; ++v) sum += red[v][threadIdx.x];
-      if (row < end && col < n1) store_y(p, row, col, sum);
-    }
-    __syncthreads();
   }
 }
 
@@ -329,8 +285,20 @@ __device__ __forceinline__ void stage_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// First row and column of tile id: bands of eight row tiles, rows first within a band.
+template <class S>
+__device__ __forceinline__ void tile_place(int id, int rows, int n_tiles, int &m0, int &n0) {
+  const int m_tiles = fp8::ceil_div(rows, S::BM);
+  const int band = uniform(id / (8 * n_tiles)), in = id - band * 8 * n_tiles;
+  const int high = m_tiles - band * 8 < 8 ? m_tiles - band * 8 : 8;
+  const int nt = uniform(in / high);
+  n0 = nt * S::BN;
+  m0 = (band * 8 + in - nt * high) * S::BM;
+}
+
 template <class S, Kind KIND, bool GROUPED>
-__global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const ProductArgs p) {
+__global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const ProductArgs p, const int t_main,
+                                                                    const int r_tiles, const int splits) {
   constexpr bool FP8 = is_e4m3(KIND);
   // one array a stage, each named in the unrolled loop below: the compiler then
   // knows which reads a load in flight cannot touch
@@ -364,22 +332,31 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
     const int sum = uniform(__shfl(upto, 63));
     total = (sum < rows_most ? sum : rows_most) * n_tiles;
   } else {
-    total = fp8::ceil_div(p.rows, S::BM) * n_tiles * p.splits;
+    total = t_main;
   }
   // Workgroups are dealt to the eight XCDs in turn. Each XCD takes one
-  // contiguous run of the tiles, its workgroups side by side in it, so that
-  // neighbouring tiles share rows of x and w in the XCD's cache.
-  const int xcd = (int)blockIdx.x & 7, share = total >> 3, rest = total & 7;
-  const int first = xcd * share + (xcd < rest ? xcd : rest), count = share + (xcd < rest);
-  const int stride = ((int)gridDim.x - xcd + 7) >> 3;
+  // contiguous run of the whole tiles and one of the parts, its workgroups side
+  // by side in it, so that neighbouring tiles share rows of x and w in the
+  // XCD's cache.
+  const int xcd = (int)blockIdx.x & 7, parts = r_tiles * splits;
+  auto run_of = [&](int all, int &start, int &length) {
+    const int share = all >> 3, rest = all & 7;
+    start = xcd * share + (xcd < rest ? xcd : rest);
+    length = share + (xcd < rest);
+  };
+  int first, count, first_part, part_count;
+  run_of(total, first, count);
+  run_of(parts, first_part, part_count);
+  const int stride = ((int)gridDim.x - xcd + 7) >> 3, all_count = count + part_count;
   int at = (int)blockIdx.x >> 3;
-  if (at >= count) return;
+  if (at >= all_count) return;
+  auto id_of = [&](int at) { return at < count ? first + at : total + first_part + at - count; };
 
   struct Tile {
-    int expert, m0, end, n0, part, blk0, blk1;
+    int expert, m0, end, n0, part, blk0, blk1;   // part: its slot in the workspace, -1 for a whole tile
   };
   auto locate = [&](int id) {
-    Tile t{0, 0, p.rows, 0, 0, 0, p.nb};
+    Tile t{0, 0, p.rows, 0, -1, 0, p.nb};
     if constexpr (GROUPED) {
       const int mt = uniform(id / n_tiles);
       t.n0 = (id - mt * n_tiles) * S::BN;
@@ -396,19 +373,14 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
       t.m0 = uniform(begin + left * S::BM);
       t.end = uniform(t.end);
     } else {
-      const int m_tiles = fp8::ceil_div(p.rows, S::BM), tiles = m_tiles * n_tiles;
-      t.part = uniform(id / tiles);
-      id -= t.part * tiles;
-      // bands of eight row tiles, rows first within a band
-      const int band = uniform(id / (8 * n_tiles)), in = id - band * 8 * n_tiles;
-      const int high = m_tiles - band * 8 < 8 ? m_tiles - band * 8 : 8;
-      const int nt = uniform(in / high);
-      t.n0 = nt * S::BN;
-      t.m0 = (band * 8 + in - nt * high) * S::BM;
-      if (p.splits > 1) {
-        t.blk0 = uniform((int)((int64_t)p.nb * t.part / p.splits));
-        t.blk1 = uniform((int)((int64_t)p.nb * (t.part + 1) / p.splits));
+      if (id >= total) {   // part q of tile total + r sits at slot q * r_tiles + r
+        t.part = id - total;
+        const int q = uniform(t.part / r_tiles);
+        id = total + t.part - q * r_tiles;
+        t.blk0 = uniform((int)((int64_t)p.nb * q / splits));
+        t.blk1 = uniform((int)((int64_t)p.nb * (q + 1) / splits));
       }
+      tile_place<S>(id, p.rows, n_tiles, t.m0, t.n0);
     }
     return t;
   };
@@ -520,7 +492,7 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
   const int w_at = (S::BM + wn * S::TN * 16 + w_row) * kStageRow + ((g ^ w_f) << 4);
   auto w_tile = [](int j) { return S::kPairs ? (j >> 1) * 32 * kStageRow + (j & 1) * 4 * kStageRow : j * 16 * kStageRow; };
 
-  Tile t = locate(first + at);
+  Tile t = locate(id_of(at));
   Loads loads = loads_of(t);
   issue_first(loads, t);
   for (;;) {
@@ -646,11 +618,11 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
 
     // all waves are through with the stages: the next tile's loads may go
     at += stride;
-    const bool more = at < count;
+    const bool more = at < all_count;
     const Tile done = t;
     stage_barrier<63>();
     if (more) {
-      t = locate(first + at);
+      t = locate(id_of(at));
       loads = loads_of(t);
       issue_first(loads, t);
     }
@@ -669,9 +641,20 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
     // A lane holds, of row r of each 16 rows of x, columns 8 g .. 8 g + 7 of each
     // 32 (from two tiles), or 4 g .. 4 g + 3 of each 16.
     constexpr int kWide = S::kPairs ? 8 : 4;
-    const bool part = !GROUPED && p.splits > 1, bf16 = p.y_bf16 && !part;
+    if (!GROUPED && done.part >= 0) {
+      float *to = p.part + (size_t)done.part * (S::BM * S::BN);
+#pragma unroll
+      for (int i = 0; i < S::TM; ++i)
+#pragma unroll
+        for (int j = 0; j < S::TN; ++j)
+          *reinterpret_cast<v4f *>(to + ((wm * S::TM + i) * 16 + r) * S::BN + wn * S::TN * 16 +
+                                   (S::kPairs ? j / 2 * 32 + g * 8 + j % 2 * 4 : j * 16 + g * 4)) = acc[i][j];
+      if (!more) return;
+      continue;
+    }
+    const bool bf16 = p.y_bf16;
     const bool whole = p.n % (bf16 ? kWide : 4) == 0;   // then rows of y keep the alignment that the stores need
-    uint8_t *to = part ? reinterpret_cast<uint8_t *>(p.part + (size_t)done.part * p.rows * p.n) : static_cast<uint8_t *>(p.y);
+    uint8_t *to = static_cast<uint8_t *>(p.y);
 #pragma unroll
     for (int i = 0; i < S::TM; ++i) {
       const int row = done.m0 + (wm * S::TM + i) * 16 + r;
@@ -711,56 +694,79 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
   }
 }
 
-// y of a product split along k: the parts in the order of k.
-__global__ __launch_bounds__(256) void product_sum_kernel(const float *__restrict__ part, const ProductArgs p) {
-  const size_t count = (size_t)p.rows * p.n;
-  const size_t at = (size_t)blockIdx.x * 256 + threadIdx.x;
-  if (at >= count) return;
-  float v = part[at];
-  for (int s = 1; s < p.splits; ++s) v += part[(size_t)s * count + at];
-  if (p.y_bf16)
-    static_cast<__bf16 *>(p.y)[at] = (__bf16)v;
-  else
-    static_cast<float *>(p.y)[at] = v;
+// y of the tiles that were cut along k: the parts in the order of k, four
+// columns a thread.
+template <class S>
+__global__ __launch_bounds__(256) void product_sum_kernel(const ProductArgs p, const int t_main, const int r_tiles,
+                                                          const int splits) {
+  constexpr int kQuads = S::BM * S::BN / 4;
+  const int in = ((int)blockIdx.x * 256 + (int)threadIdx.x) % kQuads;
+  const int tile = uniform(((int)blockIdx.x * 256 + (int)threadIdx.x) / kQuads);   // whole blocks to a tile
+  int m0, n0;
+  tile_place<S>(t_main + tile, p.rows, fp8::ceil_div(p.n, S::BN), m0, n0);
+  const int row = m0 + in / (S::BN / 4), col = n0 + in % (S::BN / 4) * 4;
+  if (row >= p.rows || col >= p.n) return;
+  const v4f *from = reinterpret_cast<const v4f *>(p.part) + (size_t)tile * kQuads + in;
+  v4f v = *from;
+  for (int s = 1; s < splits; ++s) v += from[(size_t)s * r_tiles * kQuads];
+  const size_t at = (size_t)row * p.n + col;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (col + e < p.n) {
+      if (p.y_bf16)
+        static_cast<__bf16 *>(p.y)[at + e] = (__bf16)v[e];
+      else
+        static_cast<float *>(p.y)[at + e] = v[e];
+    }
 }
 
-using Tile32 = Shape<32, 64, 1, 4, 4>;
+using Tile32 = Shape<32, 64, 1, 4, 3>;
 using Tile64 = Shape<64, 128, 1, 4, 3>;
 using Tile128 = Shape<128, 128, 4, 2, 4>;
 using Tile256 = Shape<256, 128, 4, 2, 3>;
 using Tile256Wide = Shape<256, 256, 2, 4, 2>;
 
-template <class S, Kind KIND, bool GROUPED>
-int launch_tile(const ProductArgs &a, hipStream_t s) {
-  const int64_t row_tiles = GROUPED ? fp8::grouped_row_tiles(a.rows, a.n_experts, S::BM) : fp8::ceil_div(a.rows, S::BM);
-  const int64_t tiles = row_tiles * fp8::ceil_div(a.n, S::BN) * a.splits, most = (int64_t)S::kPerCu * fp8::kSlots;
-  return launch_kernel("product_tile_kernel", product_tile_kernel<S, KIND, GROUPED>,
-                       dim3((unsigned)(tiles < most ? tiles : most)), dim3(S::kThreads), 0, s, a);
+template <class S>
+unsigned grid_of(int64_t tiles) {
+  const int64_t most = (int64_t)S::kPerCu * fp8::kSlots;
+  return (unsigned)(tiles < most ? tiles : most);
 }
 
-template <Kind KIND, bool GROUPED>
-int launch_tiles(int tile, const ProductArgs &a, hipStream_t s) {
+template <class S, Kind KIND>
+int launch_dense(const ProductArgs &a, const fp8::DensePlan &plan, hipStream_t s) {
+  const int rc = launch_kernel("product_tile_kernel", product_tile_kernel<S, KIND, false>,
+                               dim3(grid_of<S>((int64_t)plan.t_main + (int64_t)plan.r_tiles * plan.splits)),
+                               dim3(S::kThreads), 0, s, a, plan.t_main, plan.r_tiles, plan.splits);
+  if (rc || plan.r_tiles == 0) return rc;
+  return launch_kernel("product_sum_kernel", product_sum_kernel<S>, dim3((unsigned)(plan.r_tiles * (S::BM * S::BN / 1024))),
+                       dim3(256), 0, s, a, plan.t_main, plan.r_tiles, plan.splits);
+}
+
+template <class S, Kind KIND>
+int launch_grouped(const ProductArgs &a, hipStream_t s) {
+  const int64_t tiles = fp8::grouped_row_tiles(a.rows, a.n_experts, S::BM) * fp8::ceil_div(a.n, S::BN);
+  return launch_kernel("product_tile_kernel", product_tile_kernel<S, KIND, true>, dim3(grid_of<S>(tiles)),
+                       dim3(S::kThreads), 0, s, a, 0, 0, 1);
+}
+
+template <Kind KIND>
+int launch_grouped(int tile, const ProductArgs &a, hipStream_t s) {
   switch (tile) {
-    case fp8::kTile32: return launch_tile<Tile32, KIND, GROUPED>(a, s);
-    case fp8::kTile64: return launch_tile<Tile64, KIND, GROUPED>(a, s);
-    case fp8::kTile128: return launch_tile<Tile128, KIND, GROUPED>(a, s);
-    case fp8::kTile256: return launch_tile<Tile256, KIND, GROUPED>(a, s);
-    default:
-      if constexpr (KIND != kExact) return launch_tile<Tile256Wide, KIND, GROUPED>(a, s);
-      set_error_detail("product_tile_kernel", 0, "no such tile");
-      return QMV_ERR_HIP;
+    case fp8::kTile32: return launch_grouped<Tile32, KIND>(a, s);
+    case fp8::kTile64: return launch_grouped<Tile64, KIND>(a, s);
+    case fp8::kTile128: return launch_grouped<Tile128, KIND>(a, s);
+    case fp8::kTile256: return launch_grouped<Tile256, kExact>(a, s);         // fp32 results of e4m3
+    default: return launch_grouped<Tile256Wide, KIND == kBf16 ? kBf16 : kNative>(a, s);
   }
 }
 
-template <Kind KIND, bool GROUPED>
 int launch_stream(const ProductArgs &a, hipStream_t s) {
-  const int slots = GROUPED ? (a.rows < a.n_experts ? a.rows : a.n_experts) : 1;
-  const fp8::StreamPlan plan = fp8::stream_plan(a.n, a.nb, slots);
-  const dim3 grid((unsigned)fp8::ceil_div(a.n, plan.tile), (unsigned)slots);
+  const fp8::StreamPlan plan = fp8::stream_plan(a.rows, a.n, a.nb);
+  const dim3 grid((unsigned)fp8::ceil_div(a.n, plan.tile), (unsigned)fp8::ceil_div(a.rows, 16));
   switch (plan.waves) {
-    case 16: return launch_kernel("product_stream_kernel", product_stream_kernel<KIND, GROUPED, 16>, grid, dim3(1024), 0, s, a, plan.tile);
-    case 8: return launch_kernel("product_stream_kernel", product_stream_kernel<KIND, GROUPED, 8>, grid, dim3(512), 0, s, a, plan.tile);
-    default: return launch_kernel("product_stream_kernel", product_stream_kernel<KIND, GROUPED, 4>, grid, dim3(256), 0, s, a, plan.tile);
+    case 16: return launch_kernel("fp8_stream_kernel", fp8_stream_kernel<16>, grid, dim3(1024), 0, s, a, plan.tile);
+    case 8: return launch_kernel("fp8_stream_kernel", fp8_stream_kernel<8>, grid, dim3(512), 0, s, a, plan.tile);
+    default: return launch_kernel("fp8_stream_kernel", fp8_stream_kernel<4>, grid, dim3(256), 0, s, a, plan.tile);
   }
 }
 
@@ -769,25 +775,28 @@ int launch_stream(const ProductArgs &a, hipStream_t s) {
 int launch_fp8_dense(const ProductArgs &a, void *stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   const fp8::DensePlan plan = fp8::dense_plan(a.rows, a.n, a.k_bytes, a.y_bf16);
-  if (plan.stream) return launch_stream<kExact, false>(a, s);
-  const int rc = a.y_bf16 ? launch_tiles<kNative, false>(plan.tile, a, s) : launch_tiles<kExact, false>(plan.tile, a, s);
-  if (rc || a.splits == 1) return rc;
-  const unsigned grid = (unsigned)(((size_t)a.rows * a.n + 255) / 256);
-  return launch_kernel("product_sum_kernel", product_sum_kernel, dim3(grid), dim3(256), 0, s,
-                       static_cast<const float *>(a.part), a);
+  if (plan.stream) return launch_stream(a, s);
+  switch (plan.tile) {
+    case fp8::kTile32:
+      return a.y_bf16 ? launch_dense<Tile32, kNative>(a, plan, s) : launch_dense<Tile32, kExact>(a, plan, s);
+    case fp8::kTile64:
+      return a.y_bf16 ? launch_dense<Tile64, kNative>(a, plan, s) : launch_dense<Tile64, kExact>(a, plan, s);
+    case fp8::kTile128:
+      return a.y_bf16 ? launch_dense<Tile128, kNative>(a, plan, s) : launch_dense<Tile128, kExact>(a, plan, s);
+    case fp8::kTile256:
+      return a.y_bf16 ? launch_dense<Tile256, kNative>(a, plan, s) : launch_dense<Tile256, kExact>(a, plan, s);
+    default: return launch_dense<Tile256Wide, kNative>(a, plan, s);
+  }
 }
 
 int launch_fp8_grouped(const ProductArgs &a, void *stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const fp8::GroupedPlan plan = fp8::grouped_plan(a.rows, a.n_experts, !a.y_bf16);
-  if (plan.stream) return launch_stream<kExact, true>(a, s);
-  return a.y_bf16 ? launch_tiles<kNative, true>(plan.tile, a, s) : launch_tiles<kExact, true>(plan.tile, a, s);
+  const int tile = fp8::grouped_tile(a.rows, a.n_experts, !a.y_bf16);
+  return a.y_bf16 ? launch_grouped<kNative>(tile, a, s) : launch_grouped<kExact>(tile, a, s);
 }
 
 int launch_bf16_grouped(const ProductArgs &a, void *stream) {
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  const fp8::GroupedPlan plan = fp8::grouped_plan(a.rows, a.n_experts, false);
-  return plan.stream ? launch_stream<kBf16, true>(a, s) : launch_tiles<kBf16, true>(plan.tile, a, s);
+  return launch_grouped<kBf16>(fp8::grouped_tile(a.rows, a.n_experts, false), a, static_cast<hipStream_t>(stream));
 }
 
 }  // namespace qmv
