@@ -40,8 +40,9 @@ struct DensePlan {
 };
 
 // The streaming kernel reads the weights once per 16 rows of x, from the L2
-// after the first; up to here that is quicker than tiles and their parts
-// (1 x 4096 x 4096: 8 us against 15; 1 x 17408 x 5120: 26 against 20).
+// after the first. Up to 16 rows it always wins (1 x 17408 x 5120: 22.9 us
+// against 26.9 by tiles of 32 rows); with more of them while the weights are
+// small (77 x 1000 x 2064: 8 us against 14; 32 x 17408 x 5120: 56 against 33).
 constexpr int64_t kStreamBytes = (int64_t)32 << 20;
 
 inline DensePlan split_plan(int tile, int m, int n, int nb) {
@@ -64,8 +65,8 @@ inline size_t split_bytes(const DensePlan &p) {
 
 inline DensePlan dense_plan(int m, int n, int k, bool y_bf16) {
   const int nb = blocks_of(k);
-  if ((int64_t)n * k * ceil_div(m, 16) < kStreamBytes) return DensePlan{true, kTile32, 0, 0, 1};
-  if (m <= 128) return split_plan(m <= 32 ? kTile32 : m <= 64 ? kTile64 : kTile128, m <= 32 ? 32 : m, n, nb);
+  if (m <= QMM_SAME_ROWS || (int64_t)n * k * ceil_div(m, 16) < kStreamBytes) return DensePlan{true, kTile32, 0, 0, 1};
+  if (m <= 128) return split_plan(m <= 32 ? kTile32 : m <= 64 ? kTile64 : kTile128, m, n, nb);
   // Of the large tiles the one with the least time by this model, in ns: a step
   // of one block of k takes, with every CU at work, 1800 (256 x 256), 1150
   // (256 x 128) and 750 (128 x 128), in fp32 results 2200 and 1300; a tile
@@ -89,10 +90,11 @@ inline DensePlan dense_plan(int m, int n, int k, bool y_bf16) {
 inline size_t dense_workspace(int m, int n, int k, bool y_bf16) { return split_bytes(dense_plan(m, n, k, y_bf16)); }
 
 // The streaming kernel: `tile` weight rows (a multiple of four, so that a
-// lane's four results lie under one scale) and `waves` waves a workgroup, one
-// for each 16 rows of x. The tile is the one of 16, 12 and 8 rows that spreads
-// the workgroups most evenly over the CUs; with few rows, shorter tiles keep
-// every CU at work.
+// lane's four results lie under one scale; above 16, two fragments a wave) and
+// `waves` waves a workgroup, one workgroup for each 16 rows of x. The tile is
+// the one of 8 to 32 rows that spreads the workgroups most evenly over the CUs
+// (a longer one unless a shorter is 5 % better); with few rows, shorter tiles
+// keep every CU at work.
 struct StreamPlan {
   int tile, waves;
 };
@@ -101,9 +103,9 @@ inline StreamPlan stream_plan(int m, int n, int nb) {
   const int chunks = ceil_div(m, 16);   // one for every m that shares its bits
   int tile = 4;
   int64_t best_num = 0, best_den = 1, per_cu = 1;
-  for (int t = 16; t >= 8; t -= 4) {
+  for (int t = 32; t >= 8; t -= 4) {
     const int64_t groups = (int64_t)ceil_div(n, t) * chunks, rounds = (groups + kSlots - 1) / kSlots;
-    if (groups * best_den > best_num * rounds * kSlots) {   // share of the CUs' rounds that has work
+    if (groups * best_den * 20 > best_num * rounds * kSlots * 21) {   // share of the CUs' rounds that has work
       best_num = groups;
       best_den = rounds * kSlots;
       per_cu = rounds;

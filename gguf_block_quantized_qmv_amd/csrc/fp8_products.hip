@@ -116,22 +116,25 @@ __device__ __forceinline__ void expert_rows(const int32_t *__restrict__ offsets,
 
 // ---- a few rows: stream the weights ---------------------------------------------
 //
-// A workgroup owns `tile` <= 16 rows of w and 16 rows of x; wave v takes blocks
-// v, v + NW, ... of k straight from memory into MFMA fragments (no LDS), kDepth
-// blocks in flight, and the waves' sums are added in wave order: no second
-// launch. The host chooses the tile so that every CU gets the same number of
-// workgroups (a tile shorter than 16 rows repeats its last row: matrix work, no
-// memory traffic). The order of the sums goes by (n, k) alone and the columns
-// of an MFMA do not mix, so a row of x has the same bits in any company. Bound
-// by the latency of a few rounds of loads and, from some megabytes of weights
-// on, by what a CU takes from the L2 (w and x alike: a tile of 16 rows reads as
-// many bytes of x as of w).
-constexpr int kDepth = 3;
-
-template <int NW>
+// A workgroup owns `tile` <= 16 MW rows of w and 16 rows of x; wave v takes
+// blocks v, v + NW, ... of k straight from memory into MFMA fragments (no LDS),
+// DEPTH blocks in flight, and the waves' sums are added in wave order: no
+// second launch. The host chooses the tile so that every CU gets the same number
+// of workgroups (a fragment of fewer than 16 rows repeats its last row: matrix
+// work, no memory traffic). The order of the sums goes by (n, k) alone and the columns
+// of an MFMA do not mix, so a row of x has the same bits in any company.
+//
+// Bound by the weight stream: 1 x 17408 x 5120 takes 17.4 us with the weights
+// partly in the last-level cache (5.1 TB/s; a plain read of as many bytes 17.6
+// us from HBM) and 22.9 us from HBM. What counted: two fragments of w for one
+// of x (MW = 1 reads as many bytes of x as of w through the L2: 26.5 us), and
+// plain loads (a fragment takes a 128-byte line in two halves: with
+// non-temporal loads each half fetched the line, 23.7 us). Matrices of less
+// than 32 rows a CU take MW = 1 and shorter tiles: 1 x 4096 x 4096 8 us.
+template <int NW, int MW, int DEPTH>
 __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) void fp8_stream_kernel(
     const ProductArgs p, const int tile) {
-  __shared__ float red[NW][256];
+  __shared__ float red[NW][MW * 256];
   const int lane = (int)threadIdx.x & 63, wave = uniform((int)threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int n0 = (int)blockIdx.x * tile, n1 = n0 + tile < p.n ? n0 + tile : p.n;
@@ -139,81 +142,101 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
   // Lane offsets from scalar addresses. They are hidden from the optimiser at
   // every use, which would otherwise keep one 64-bit address per block alive.
   const uint8_t *wbase = p.w + (size_t)n0 * p.k_bytes, *xbase = p.x + (size_t)m0 * p.k_bytes;
-  uint32_t wlane = (uint32_t)(n0 + r < n1 ? r : n1 - 1 - n0) * (uint32_t)p.k_bytes + g * 16;
+  uint32_t wlane[MW], wslane[MW];
+#pragma unroll
+  for (int i = 0; i < MW; ++i) {
+    const int row = n0 + i * 16 + r, srow = n0 + i * 16 + g * 4;
+    wlane[i] = (uint32_t)((row < n1 ? row : n1 - 1) - n0) * (uint32_t)p.k_bytes + g * 16;
+    // tiles are multiples of four rows: a lane's four results share a scale
+    wslane[i] = (uint32_t)((srow < p.n ? srow : p.n - 1) >> 7) * (uint32_t)p.nb;
+  }
   uint32_t xlane = (uint32_t)(m0 + r < m1 ? r : m1 - 1 - m0) * (uint32_t)p.k_bytes + g * 16;
-  // tiles are multiples of four rows: a lane's four results share a scale
-  const int srow = n0 + g * 4 < p.n ? n0 + g * 4 : p.n - 1;
-  uint32_t wslane = (uint32_t)(srow >> 7) * (uint32_t)p.nb;
   uint32_t xslane = (uint32_t)(m0 + r < m1 ? m0 + r : m1 - 1);
   const int whole = p.k_bytes >> 7, tail = p.k_bytes & 127;
 
-  Frag wf[kDepth], xf[kDepth];
-  float xs[kDepth], ws[kDepth];
+  Frag wf[DEPTH][MW], xf[DEPTH];
+  float xs[DEPTH], ws[DEPTH][MW];
   // Block b (past the last whole one: zeros, so that every pass of the loop
   // sends the same loads and each wait counts exactly those behind it).
   auto load_scales = [&](int b, int u, bool ok) {
-    asm("" : "+v"(xslane), "+v"(wslane));
     const float *zeros = reinterpret_cast<const float *>(g_zeros);
+    asm("" : "+v"(xslane));
     xs[u] = (ok ? p.x_scale + (size_t)b * p.x_rows : zeros)[ok ? xslane : 0];
-    ws[u] = (ok ? p.w_scale + b : zeros)[ok ? wslane : 0];
+#pragma unroll
+    for (int i = 0; i < MW; ++i) {
+      asm("" : "+v"(wslane[i]));
+      ws[u][i] = (ok ? p.w_scale + b : zeros)[ok ? wslane[i] : 0];
+    }
   };
   auto load = [&](int b, int u) {
-    asm("" : "+v"(wlane), "+v"(xlane));
     const bool ok = b < whole;
     const uint8_t *zeros = reinterpret_cast<const uint8_t *>(g_zeros);
-    const uint8_t *w = (ok ? wbase + (size_t)b * 128 : zeros) + (ok ? wlane : 0);
+#pragma unroll
+    for (int i = 0; i < MW; ++i) {
+      asm("" : "+v"(wlane[i]));
+      const uint8_t *w = (ok ? wbase + (size_t)b * 128 : zeros) + (ok ? wlane[i] : 0);
+      wf[u][i].lo = *reinterpret_cast<const v4i *>(w);
+      wf[u][i].hi = *reinterpret_cast<const v4i *>(w + 64);
+    }
+    asm("" : "+v"(xlane));
     const uint8_t *x = (ok ? xbase + (size_t)b * 128 : zeros) + (ok ? xlane : 0);
-    wf[u].lo = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(w));
-    wf[u].hi = __builtin_nontemporal_load(reinterpret_cast<const v4i *>(w + 64));
     xf[u].lo = *reinterpret_cast<const v4i *>(x);
     xf[u].hi = *reinterpret_cast<const v4i *>(x + 64);
     load_scales(b, u, ok);
   };
-  v4f acc = kZero4;
+  v4f acc[MW];
+#pragma unroll
+  for (int i = 0; i < MW; ++i) acc[i] = kZero4;
   auto use = [&](int u) {
-    Operand<kExact> a, c;
-    a.set(wf[u]);
+    Operand<kExact> c;
     c.set(xf[u]);
-    scaled_add(xs[u] * ws[u], mma_block<kExact>(a, c, kZero4), acc);
+#pragma unroll
+    for (int i = 0; i < MW; ++i) {
+      Operand<kExact> a;
+      a.set(wf[u][i]);
+      scaled_add(xs[u] * ws[u][i], mma_block<kExact>(a, c, kZero4), acc[i]);
+    }
   };
 #pragma unroll
-  for (int u = 0; u < kDepth; ++u) load(wave + u * NW, u);
-  for (int b = wave; b < whole; b += kDepth * NW)
+  for (int u = 0; u < DEPTH; ++u) load(wave + u * NW, u);
+  for (int b = wave; b < whole; b += DEPTH * NW)
 #pragma unroll
-    for (int u = 0; u < kDepth; ++u) {
+    for (int u = 0; u < DEPTH; ++u) {
       use(u);
-      load(b + (u + kDepth) * NW, u);
+      load(b + (u + DEPTH) * NW, u);
       __builtin_amdgcn_sched_barrier(0);   // one block's widened operands at a time
     }
   if (tail && wave == whole % NW) {   // the partial last block: zeros past the row
     const v4i none = {0, 0, 0, 0};
-    wf[0].lo = wf[0].hi = xf[0].lo = xf[0].hi = none;
-    const uint8_t *w = wbase + (size_t)whole * 128 + wlane, *x = xbase + (size_t)whole * 128 + xlane;
-    if (g * 16 < tail) {
-      wf[0].lo = *reinterpret_cast<const v4i *>(w);
-      xf[0].lo = *reinterpret_cast<const v4i *>(x);
-    }
-    if (g * 16 + 64 < tail) {
-      wf[0].hi = *reinterpret_cast<const v4i *>(w + 64);
-      xf[0].hi = *reinterpret_cast<const v4i *>(x + 64);
+    const uint8_t *x = xbase + (size_t)whole * 128 + xlane;
+    xf[0].lo = xf[0].hi = none;
+    if (g * 16 < tail) xf[0].lo = *reinterpret_cast<const v4i *>(x);
+    if (g * 16 + 64 < tail) xf[0].hi = *reinterpret_cast<const v4i *>(x + 64);
+#pragma unroll
+    for (int i = 0; i < MW; ++i) {
+      const uint8_t *w = wbase + (size_t)whole * 128 + wlane[i];
+      wf[0][i].lo = wf[0][i].hi = none;
+      if (g * 16 < tail) wf[0][i].lo = *reinterpret_cast<const v4i *>(w);
+      if (g * 16 + 64 < tail) wf[0][i].hi = *reinterpret_cast<const v4i *>(w + 64);
     }
     load_scales(whole, 0, true);
     use(0);
   }
-  // lane l holds columns 4 g .. 4 g + 3 of row r of x
-  *reinterpret_cast<v4f *>(&red[wave][r * 16 + g * 4]) = acc;
-  __syncthreads();
-  if ((int)threadIdx.x < 256) {
-    const int row = m0 + ((int)threadIdx.x >> 4), col = n0 + ((int)threadIdx.x & 15);
-    float sum = red[0][threadIdx.x];
+  // lane l holds columns 4 g .. 4 g + 3 of each 16 of row r of x
 #pragma unroll
-    for (int v = 1; v < NW; ++v) sum += red[v][threadIdx.x];
+  for (int i = 0; i < MW; ++i) *reinterpret_cast<v4f *>(&red[wave][(r * MW + i) * 16 + g * 4]) = acc[i];
+  __syncthreads();
+  for (int at = (int)threadIdx.x; at < MW * 256; at += NW * 64) {
+    const int row = m0 + at / (MW * 16), col = n0 + at % (MW * 16);
+    float sum = red[0][at];
+#pragma unroll
+    for (int v = 1; v < NW; ++v) sum += red[v][at];
     if (row < m1 && col < n1) {
-      const size_t at = (size_t)row * p.n + col;
+      const size_t to = (size_t)row * p.n + col;
       if (p.y_bf16)
-        static_cast<__bf16 *>(p.y)[at] = (__bf16)sum;
+        static_cast<__bf16 *>(p.y)[to] = (__bf16)sum;
       else
-        static_cast<float *>(p.y)[at] = sum;
+        static_cast<float *>(p.y)[to] = sum;
     }
   }
 }
@@ -760,14 +783,20 @@ int launch_grouped(int tile, const ProductArgs &a, hipStream_t s) {
   }
 }
 
+template <int MW>
+int launch_stream(const ProductArgs &a, const fp8::StreamPlan &plan, hipStream_t s) {
+  const dim3 grid((unsigned)fp8::ceil_div(a.n, plan.tile), (unsigned)fp8::ceil_div(a.rows, 16));
+  constexpr int kDepth = MW == 1 ? 3 : 2;
+  switch (plan.waves) {
+    case 16: return launch_kernel("fp8_stream_kernel", fp8_stream_kernel<16, MW, kDepth>, grid, dim3(1024), 0, s, a, plan.tile);
+    case 8: return launch_kernel("fp8_stream_kernel", fp8_stream_kernel<8, MW, kDepth>, grid, dim3(512), 0, s, a, plan.tile);
+    default: return launch_kernel("fp8_stream_kernel", fp8_stream_kernel<4, MW, kDepth>, grid, dim3(256), 0, s, a, plan.tile);
+  }
+}
+
 int launch_stream(const ProductArgs &a, hipStream_t s) {
   const fp8::StreamPlan plan = fp8::stream_plan(a.rows, a.n, a.nb);
-  const dim3 grid((unsigned)fp8::ceil_div(a.n, plan.tile), (unsigned)fp8::ceil_div(a.rows, 16));
-  switch (plan.waves) {
-    case 16: return launch_kernel("fp8_stream_kernel", fp8_stream_kernel<16>, grid, dim3(1024), 0, s, a, plan.tile);
-    case 8: return launch_kernel("fp8_stream_kernel", fp8_stream_kernel<8>, grid, dim3(512), 0, s, a, plan.tile);
-    default: return launch_kernel("fp8_stream_kernel", fp8_stream_kernel<4>, grid, dim3(256), 0, s, a, plan.tile);
-  }
+  return plan.tile > 16 ? launch_stream<2>(a, plan, s) : launch_stream<1>(a, plan, s);
 }
 
 }  // namespace

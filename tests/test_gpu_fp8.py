@@ -171,22 +171,24 @@ def test_dense(q, dev, m, n, k, out):
     check(host(y.double()), exact, bound(mag, k, out, exact))
 
 
-def test_dense_large_tiles(q, dev):
-    # enough 256 x 256 tiles for the largest shape; rows and columns end inside the last ones
-    m, n, k = 4000, 4211, 400
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("m,n,k", [(4000, 4211, 400), (4000, 4216, 400), (8200, 2560, 256), (300, 17000, 1168),
+                                   (700, 4096, 2304), (40, 20000, 2000), (24, 9000, 4096), (100, 30000, 640)])
+def test_dense_large_tiles(q, dev, out, m, n, k):
+    # whole rounds of tiles and rounds cut along k, in every tile shape; rows and columns end inside the last tiles
     w, ws, x, xs = dense_case(1, m, n, k)
-    y, buf = guarded((m, n), torch.float32, dev)
-    q.qmm_fp8(up(w, dev), up(ws, dev), up(x, dev), up(xs, dev), n, k, y=y)
+    args = up(w, dev), up(ws, dev), up(x, dev), up(xs, dev), n, k
+    y, buf = guarded((m, n), out, dev)
+    q.qmm_fp8(*args, y=y)
     torch.cuda.synchronize()
     assert guards_intact(buf)
-    pick = rng(4).choice(m, 150, replace=False)
+    pick = np.unique(np.concatenate([rng(4).choice(m, min(m, 60), replace=False), [0, m - 1]]))
     exact, mag = o.product(o.rows_f64(x[pick], xs[:, pick]), o.weights_f64(w, ws))
-    check(host(y)[pick].astype(np.float64), exact, bound(mag, k, torch.float32, exact))
-    again = q.qmm_fp8(up(w, dev), up(ws, dev), up(x, dev), up(xs, dev), n, k)
-    assert torch.equal(again.view(torch.int32), y.view(torch.int32))
+    check(host(y.double())[pick], exact, bound(mag, k, out, exact))
+    assert torch.equal(q.qmm_fp8(*args, out_dtype=out), y)
 
 
-@pytest.mark.parametrize("n,k", [(130, 256), (100, 2064), (48, 8192)])
+@pytest.mark.parametrize("n,k", [(130, 256), (100, 2064), (48, 8192), (6004, 528), (4100, 9216)])
 def test_dense_rows_have_the_same_bits_in_any_company(q, dev, n, k):
     w, ws, x, xs = dense_case(2, 16, n, k)
     wd, wsd = up(w, dev), up(ws, dev)
@@ -237,6 +239,7 @@ GROUPS = [
     ([1], 16, 128, 1, False, 0, 0), ([0, 0, 3, 0], 17, 144, 2, True, 0, 0), ([1, 0, 2, 1, 0, 1], 130, 1040, 4, True, 0, 3),
     ([5, 0, 40, 0, 0, 1, 2], 100, 400, 30, True, 2, 1), ([20, 33, 0, 31], 129, 256, 50, False, 0, 5),
     ([64, 1, 65, 90], 257, 272, 70, True, 0, 0), ([300, 0, 129], 140, 384, 200, True, 1, 7), ([0, 0], 40, 128, 3, True, 2, 2),
+    ([400, 3, 0, 700, 257], 520, 640, 300, True, 0, 2), ([256] * 40, 264, 384, 500, False, 0, 0),
     ([3] * 70 + [0] * 60 + [1], 24, 128, 9, True, 0, 0), ([40] * 70, 24, 128, 9, True, 0, 0),
 ]
 
