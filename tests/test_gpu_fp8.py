@@ -304,3 +304,172 @@ def test_grouped_no_rows_and_fresh_output(q, dev, kind):
     off, index, data, _, _ = grouped_case(3, kind, [2, 0, 1], 24, 128, 4, True, spare=2)
     y = host(run_grouped(q, dev, kind, off, index, data, 24, 128, None))
     assert (y[3:] == 0).all() and (y[:3] != 0).any()
+
+
+# ------------------------------------------------------------------ as a program uses them
+
+def ffn_case(seed, dev, t, hidden, ffn, e, top):
+    """A routed feed-forward layer with e4m3 experts: weights, token rows and the routing a program computes with torch."""
+    g = rng(6, seed)
+    gate_up, gs = codes8(g, e, 2 * ffn, hidden), scales(g, e, o.blocks(2 * ffn), o.blocks(hidden)) * 1e-3
+    down, ds = codes8(g, e, hidden, ffn), scales(g, e, o.blocks(hidden), o.blocks(ffn)) * 1e-3
+    x = torch.from_numpy(g.standard_normal((t, hidden)).astype(np.float32)).to(torch.bfloat16)
+    ids = torch.from_numpy(np.stack([g.choice(e, top, replace=False) for _ in range(t)]).astype(np.int64))
+    weight = torch.softmax(torch.from_numpy(g.standard_normal((t, top)).astype(np.float32)), 1)
+    order = torch.argsort(ids.flatten(), stable=True)
+    counts = torch.bincount(ids.flatten(), minlength=e)
+    offsets = torch.cat([counts.new_zeros(1), counts.cumsum(0)]).to(torch.int32)
+    host_side = (gate_up, gs, down, ds, x, ids, weight)
+    on_dev = tuple(up(a, dev) for a in (gate_up, gs, down, ds)) + (x.to(dev), offsets.to(dev), (order // top).to(torch.int32).to(dev),
+                                                              order.to(dev), weight.to(dev))
+    return host_side, on_dev
+
+
+def run_ffn(q, d, hidden, ffn, top, stream=None):
+    gate_up, gs, down, ds, x, offsets, token, order, weight = d
+    xq, xs = q.qmm_fp8_quant(x, stream=stream)
+    gu = q.qmm_fp8_grouped(gate_up, gs, xq, xs, offsets, 2 * ffn, hidden, row_index=token, stream=stream)
+    hq, hs = q.qmm_fp8_quant_silu_mul(gu, stream=stream)
+    z = q.qmm_fp8_grouped(down, ds, hq, hs, offsets, hidden, ffn, stream=stream)
+    y = torch.zeros_like(z)
+    y[order] = z                                             # back to token order, rank after rank
+    return (y.view(-1, top, hidden) * weight[:, :, None]).sum(1), (xq, xs, gu, hq, hs, z)
+
+
+@pytest.mark.parametrize("t,hidden,ffn,e,top", [(1, 256, 128, 8, 2), (5, 400, 144, 6, 3), (70, 512, 256, 16, 4),
+                                                (300, 512, 128, 3, 2)])
+def test_routed_ffn_of_e4m3_experts(q, dev, t, hidden, ffn, e, top):
+    h, d = ffn_case(t, dev, t, hidden, ffn, e, top)
+    got, (xq, xs, gu, hq, hs, z) = run_ffn(q, d, hidden, ffn, top)
+    gate_up, gs, down, ds, x, ids, weight = h
+    token = host(d[6])
+    # each step against fp64 on the step's own inputs
+    codes, s = o.quant(x.float().numpy())
+    assert np.array_equal(host(xs), s) and np.array_equal(o.decode(host(xq.view(torch.uint8))), o.decode(codes))
+    off = host(d[5])
+    wg = [o.weights_f64(gate_up[i], gs[i]) for i in range(e)]
+    exact, mag = o.grouped(o.rows_f64(codes, s), wg, off, np.zeros((t * top, 2 * ffn)), token)
+    check(host(gu.double()), exact, bound(mag, hidden, torch.float32, exact))
+    hf = o.silu_mul(host(gu.double()))
+    row = np.repeat(host(hs).astype(np.float64).T, 128, axis=1)[:, :ffn]
+    hd = o.decode(host(hq.view(torch.uint8))) * row
+    rel = 8 * 2.0 ** -23
+    check(hd, hf, np.abs(hf) * (2.0 ** -4 + 2 * rel) + row * 2.0 ** -10 * (1 + 2 * rel) + 1e-37)
+    wd = [o.weights_f64(down[i], ds[i]) for i in range(e)]
+    exact, mag = o.grouped(hd, wd, off, np.zeros((t * top, hidden)))
+    check(host(z.double()), exact, bound(mag, ffn, torch.float32, exact))
+    assert got.shape == (t, hidden) and bool(torch.isfinite(got).all())
+
+
+def test_ffn_replayed_from_a_graph_beside_eager_calls(q, dev):
+    hidden, ffn, top = 512, 256, 4
+    _, d = ffn_case(1, dev, 40, hidden, ffn, 16, top)
+    _, other = ffn_case(2, dev, 40, hidden, ffn, 16, top)
+    gate_up, gs, down, ds, x, offsets, token, order, weight = d
+    w, ws, xd, xsd = (up(a, dev) for a in dense_case(9, 200, 3000, 2048))
+    need = q.qmm_fp8_workspace(200, 3000, 2048, torch.bfloat16)
+    assert need > 0
+    space = torch.empty(need, dtype=torch.uint8, device=dev)
+    buf = {"xq": torch.empty(40, hidden, dtype=torch.float8_e4m3fn, device=dev), "xs": torch.empty(4, 40, device=dev),
+           "gu": torch.empty(160, 2 * ffn, device=dev), "hq": torch.empty(160, ffn, dtype=torch.float8_e4m3fn, device=dev),
+           "hs": torch.empty(2, 160, device=dev), "z": torch.empty(160, hidden, dtype=torch.bfloat16, device=dev),
+           "y": torch.empty(200, 3000, dtype=torch.bfloat16, device=dev)}
+
+    def step():
+        q.qmm_fp8_quant(x, xq=buf["xq"], xs=buf["xs"])
+        q.qmm_fp8_grouped(gate_up, gs, buf["xq"], buf["xs"], offsets, 2 * ffn, hidden, row_index=token, y=buf["gu"])
+        q.qmm_fp8_quant_silu_mul(buf["gu"], xq=buf["hq"], xs=buf["hs"])
+        q.qmm_fp8_grouped(down, ds, buf["hq"], buf["hs"], offsets, hidden, ffn, y=buf["z"])
+        q.qmm_fp8(w, ws, xd, xsd, 3000, 2048, y=buf["y"], ws=space)
+
+    step()
+    torch.cuda.synchronize()
+    want = {k: v.clone() for k, v in buf.items()}
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step()
+    for _ in range(4):
+        for v in buf.values():
+            v.view(torch.uint8).fill_(0x55)
+        space.fill_(0xFF)
+        run_ffn(q, other, hidden, ffn, top)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        for k, v in want.items():
+            assert torch.equal(buf[k].view(torch.uint8), v.view(torch.uint8)), k
+
+
+def test_two_streams_at_once(q, dev):
+    # each stream has its own workspace (none given: the call allocates it); repeated, the results are the same bits
+    cases = [tuple(up(a, dev) for a in dense_case(10 + i, 300, 2500, 2048)) for i in range(2)]
+    want = [q.qmm_fp8(w, ws, x, xs, 2500, 2048, out_dtype=torch.bfloat16) for w, ws, x, xs in cases]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(5):
+        for i, (w, ws, x, xs) in enumerate(cases):
+            with torch.cuda.stream(streams[i]):
+                y = torch.empty(300, 2500, dtype=torch.bfloat16, device=dev)
+            got[i].append(q.qmm_fp8(w, ws, x, xs, 2500, 2048, y=y, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(y, want[i]) for y in got[i]), i
+
+
+def test_one_matrix_may_be_both_operands(q, dev):
+    # inputs may overlap each other: x x^T with x as the weights too, under equal scales
+    g = rng(11)
+    x = codes8(g, 128, 256)
+    xd = up(x, dev)
+    y = host(q.qmm_fp8(xd, torch.ones(1, 2, device=dev), xd, torch.ones(2, 128, device=dev), 128, 256))
+    exact, mag = o.product(o.decode(x), o.decode(x))
+    check(y.astype(np.float64), exact, bound(mag, 256, torch.float32, exact))
+
+
+def test_binding_refusals(q, dev):
+    w, ws, x, xs = (up(a, dev) for a in dense_case(12, 4, 130, 256))
+    with pytest.raises(ValueError, match="x_scale has shape"):
+        q.qmm_fp8(w, ws, x, xs.t().contiguous(), 130, 256)
+    with pytest.raises(ValueError, match="contiguous"):
+        q.qmm_fp8(w, ws.t().contiguous().t(), x, xs, 130, 256)
+    with pytest.raises(ValueError, match="w has shape"):
+        q.qmm_fp8(w, ws, x, xs, 129, 256)
+    with pytest.raises(TypeError, match="dtype"):
+        q.qmm_fp8(w, ws.double(), x, xs, 130, 256)
+    with pytest.raises(TypeError, match="out_dtype"):
+        q.qmm_fp8(w, ws, x, xs, 130, 256, y=torch.empty(4, 130, device=dev), out_dtype=torch.bfloat16)
+    with pytest.raises(TypeError, match="dtype"):
+        q.qmm_fp8(w, ws, x, xs, 130, 256, y=torch.empty(4, 130, device=dev, dtype=torch.float16))
+    with pytest.raises(ValueError, match="device memory"):
+        q.qmm_fp8(w.cpu(), ws, x, xs, 130, 256)
+    with pytest.raises(q.QmvError) as e:
+        q.qmm_fp8(w, ws, x, xs, 130, 256, ws=torch.empty(8, dtype=torch.uint8, device=dev)[4:])
+    assert e.value.code == -4                                 # the workspace is not aligned
+    off = torch.tensor([0, 2, 4], dtype=torch.int32, device=dev)
+    w3, ws3 = w[:128].reshape(2, 64, 256), ws[:1].expand(2, 2)[:, None].contiguous()
+    with pytest.raises(ValueError, match="offsets has shape"):
+        q.qmm_fp8_grouped(w3, ws3, x, xs, off[:2].contiguous(), 64, 256)
+    with pytest.raises(TypeError, match="dtype"):
+        q.qmm_fp8_grouped(w3, ws3, x, xs, off.long(), 64, 256)
+    with pytest.raises(TypeError):
+        q.qmm_fp8_grouped(w3, None, x, xs, off, 64, 256)
+    with pytest.raises(ValueError, match="w_scale has shape"):
+        q.qmm_fp8_grouped(w3, ws3[:1].contiguous(), x, xs, off, 64, 256)
+
+
+def test_grouped_bank_beyond_32_bit_offsets(q, dev):
+    # 66 experts of 64 MiB: the last one's weights begin past 4 GiB; the same bits as from its matrix alone
+    e, n, k, rows = 66, 8192, 8192, 40
+    g = torch.Generator(device=dev).manual_seed(3)
+    w = torch.randint(0, 120, (e, n, k), dtype=torch.uint8, device=dev, generator=g)
+    ws = torch.rand(e, 64, 64, device=dev, generator=g) + 0.5
+    x, xs = q.qmm_fp8_quant(torch.randn(rows, k, device=dev, generator=g))
+    off = torch.zeros(e + 1, dtype=torch.int32, device=dev)
+    off[-1] = rows
+    y = q.qmm_fp8_grouped(w, ws, x, xs, off, n, k, out_dtype=torch.bfloat16)
+    alone = q.qmm_fp8(w[-1], ws[-1], x, xs, n, k)
+    assert bool(torch.isfinite(alone).all())
+    assert torch.allclose(y.float(), alone, rtol=2.0 ** -7, atol=float(alone.abs().mean()) * 2.0 ** -7)
