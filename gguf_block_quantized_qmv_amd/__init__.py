@@ -490,7 +490,7 @@ _FLOATS = {_torch().float32: 0, _torch().bfloat16: 1}   # QMM_F32, QMM_BF16
 
 
 def _explain(t, name, types, shape, index):
-    _dev(t, name, types)
+    _dev(t, name, tuple(types))
     if tuple(t.shape) != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
     raise ValueError(f"{name} is on {t.device}, other tensors on cuda:{index}")
@@ -507,11 +507,15 @@ def _take(t, name, types, shape, index):
 
 
 def _first(x, name, types, dims):
-    """Device index and shape of the tensor that the others go by."""
-    _dev(x, name, types)
-    if x.dim() != dims:
+    """Device index and shape of the tensor that the others go by (its address is taken, and checked, later)."""
+    try:
+        index, shape = x.get_device(), x.shape
+    except AttributeError:
+        index = -1
+    if index < 0 or len(shape) != dims:
+        _dev(x, name, tuple(types))
         raise ValueError(f"{name} has {x.dim()} dimensions, expected {dims}")
-    return x.get_device(), x.shape
+    return index, shape
 
 
 def _run(fn, name, index, stream, *args):
@@ -534,7 +538,7 @@ def _run(fn, name, index, stream, *args):
 
 def _quant(fn, name, x, gated, xq, xs, stream):
     torch = _torch()
-    index, (m, k) = _first(x, "x", tuple(_FLOATS), 2)
+    index, (m, k) = _first(x, "x", _FLOATS, 2)
     if gated:
         if k % 2:
             raise ValueError(f"{name}: x must be [m, 2 k], got {(m, k)}")
@@ -543,7 +547,8 @@ def _quant(fn, name, x, gated, xq, xs, stream):
         xq = torch.empty((m, k), dtype=torch.float8_e4m3fn, device=x.device)
     if xs is None:
         xs = torch.empty((_blocks(k), m), dtype=torch.float32, device=x.device)
-    _run(fn, name, index, stream, x.data_ptr(), _FLOATS[x.dtype], _take(xq, "xq", _E4M3, (m, k), index),
+    xp = _take(x, "x", _FLOATS, x.shape, index)
+    _run(fn, name, index, stream, xp, _FLOATS[x.dtype], _take(xq, "xq", _E4M3, (m, k), index),
          _take(xs, "xs", _F32, (_blocks(k), m), index), m, k)
     return xq, xs
 

@@ -59,7 +59,7 @@ int grouped(const void *w, size_t w_bytes, const float *w_scale, const void *x, 
   const size_t wb = (size_t)n_experts * n * k * value_bytes;   // <= 2^51
   if (w_bytes != wb) return QMV_ERR_SIZE;
   if (rows == 0) return QMV_OK;
-  if (!qmv::fp8::grouped_in_grid(rows, n, n_experts, e4m3 && y_type == QMM_F32)) return QMV_ERR_RANGE;
+  if (!qmv::fp8::grouped_in_grid(rows, n_experts, n, qmv::fp8::blocks_of(k * value_bytes), e4m3 && y_type == QMM_F32)) return QMV_ERR_RANGE;
   // rows are gathered by 32-bit byte offsets
   if (row_index && (size_t)x_rows * k * value_bytes > UINT32_MAX) return QMV_ERR_RANGE;
   // with no row of x every index is out of range, and x itself may be null

@@ -44,7 +44,7 @@ struct DensePlan {
 // against 26.9 by tiles of 32 rows); with more of them while the weights are
 // small (77 x 1000 x 2064: 8 us against 14; 32 x 17408 x 5120: 56 against 33).
 constexpr int64_t kStreamBytes = (int64_t)32 << 20;
-constexpr int kStreamRows = 512;   // 512 x 1024 x 1024: 13.8 us against 14.5
+constexpr int kStreamRows = 2048;   // 512 x 1024 x 1024: 13.8 us against 14.5
 
 inline DensePlan split_plan(int tile, int m, int n, int nb) {
   DensePlan p{false, tile, 0, 0, 1};
@@ -122,10 +122,32 @@ inline StreamPlan stream_plan(int m, int n, int nb) {
 
 // ---- grouped -----------------------------------------------------------------
 
-// Host code cannot see the offsets: the tile goes by the rows spread evenly.
-inline int grouped_tile(int rows, int n_experts, bool exact) {
-  const int avg = rows / (n_experts < 1 ? 1 : n_experts);
-  return avg <= 24 ? kTile32 : avg <= 64 ? kTile64 : avg <= 128 ? kTile128 : exact ? kTile256 : kTile256Wide;
+// Host code cannot see the offsets: rows are taken as spread evenly, half a
+// tile lost at the end of each expert's run. Of the tiles the one with the
+// least time by this model, in ns: a step of one block of k takes 800 (32 x 64,
+// four workgroups a CU), 900 (64 x 128, two), 750 (128 x 128), 1150 (256 x 128)
+// and 1800 (256 x 256), in fp32 results of e4m3 up to twice that; a tile starts
+// and ends in 6000.
+inline int grouped_tile(int rows, int n_experts, int n, int nb, bool exact) {
+  const int busy = rows < n_experts ? rows : n_experts;
+  int best = kTile32;
+  int64_t least = INT64_MAX;
+  for (int tile = kTile32; tile <= (exact ? kTile256 : kTile256Wide); ++tile) {
+    if (tile == kTile256 && !exact) continue;   // 256 x 256 does better
+    const int bm = tile_rows(tile), per_cu = tile == kTile32 ? 4 : tile == kTile64 ? 2 : 1;
+    int64_t row_tiles = ((int64_t)rows + (int64_t)busy * bm / 2) / bm;
+    if (row_tiles < busy) row_tiles = busy;
+    const int64_t tiles = row_tiles * ceil_div(n, tile_cols(tile));
+    const int64_t rounds = (tiles + per_cu * kSlots - 1) / (per_cu * kSlots);
+    const int64_t step = tile == kTile32 ? (exact ? 900 : 800) : tile == kTile64 ? (exact ? 1200 : 900)
+                         : tile == kTile128 ? (exact ? 1300 : 750) : tile == kTile256 ? 2200 : 1800;
+    const int64_t cost = rounds * (nb * step + 6000);
+    if (cost < least) {
+      least = cost;
+      best = tile;
+    }
+  }
+  return best;
 }
 
 // Row tiles a grouped launch can need: every expert with rows may have one
@@ -139,8 +161,8 @@ constexpr int64_t kMaxTiles = (int64_t)1 << 28;
 
 inline bool dense_in_grid(int m, int n) { return (int64_t)ceil_div(m, 128) * ceil_div(n, 64) <= kMaxTiles; }
 
-inline bool grouped_in_grid(int rows, int n, int n_experts, bool exact) {
-  const int t = grouped_tile(rows, n_experts, exact);
+inline bool grouped_in_grid(int rows, int n_experts, int n, int nb, bool exact) {
+  const int t = grouped_tile(rows, n_experts, n, nb, exact);
   return grouped_row_tiles(rows, n_experts, tile_rows(t)) * ceil_div(n, tile_cols(t)) <= kMaxTiles;
 }
 

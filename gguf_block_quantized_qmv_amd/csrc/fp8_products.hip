@@ -676,8 +676,10 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
       continue;
     }
     const bool bf16 = p.y_bf16;
-    const bool whole = p.n % (bf16 ? kWide : 4) == 0;   // then rows of y keep the alignment that the stores need
     uint8_t *to = static_cast<uint8_t *>(p.y);
+    // vector stores to any element's address: rows of y of odd lengths keep no alignment
+    typedef __bf16 RowBf16 __attribute__((ext_vector_type(kWide), aligned(2)));
+    typedef float RowF32 __attribute__((ext_vector_type(4), aligned(4)));
 #pragma unroll
     for (int i = 0; i < S::TM; ++i) {
       const int row = done.m0 + (wm * S::TM + i) * 16 + r;
@@ -689,7 +691,7 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
 #pragma unroll
         for (int e = 0; e < kWide; ++e) v[e] = acc[i][j + e / 4][e % 4];
         const size_t place = (size_t)row * p.n + col;
-        if (!whole) {
+        if (col + kWide > p.n) {
 #pragma unroll
           for (int e = 0; e < kWide; ++e)
             if (col + e < p.n) {
@@ -699,17 +701,14 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
                 reinterpret_cast<float *>(to)[place + e] = v[e];
             }
         } else if (bf16) {
-          if (col >= p.n) continue;
-          typedef __bf16 Row __attribute__((ext_vector_type(kWide)));
-          Row o;
+          RowBf16 o;
 #pragma unroll
           for (int e = 0; e < kWide; ++e) o[e] = (__bf16)v[e];
-          *reinterpret_cast<Row *>(reinterpret_cast<__bf16 *>(to) + place) = o;
+          *reinterpret_cast<RowBf16 *>(reinterpret_cast<__bf16 *>(to) + place) = o;
         } else {
 #pragma unroll
           for (int e = 0; e < kWide; e += 4)
-            if (col + e < p.n)
-              *reinterpret_cast<v4f *>(reinterpret_cast<float *>(to) + place + e) = v4f{v[e], v[e + 1], v[e + 2], v[e + 3]};
+            *reinterpret_cast<RowF32 *>(reinterpret_cast<float *>(to) + place + e) = RowF32{v[e], v[e + 1], v[e + 2], v[e + 3]};
         }
       }
     }
@@ -820,12 +819,12 @@ int launch_fp8_dense(const ProductArgs &a, void *stream) {
 
 int launch_fp8_grouped(const ProductArgs &a, void *stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const int tile = fp8::grouped_tile(a.rows, a.n_experts, !a.y_bf16);
+  const int tile = fp8::grouped_tile(a.rows, a.n_experts, a.n, a.nb, !a.y_bf16);
   return a.y_bf16 ? launch_grouped<kNative>(tile, a, s) : launch_grouped<kExact>(tile, a, s);
 }
 
 int launch_bf16_grouped(const ProductArgs &a, void *stream) {
-  return launch_grouped<kBf16>(fp8::grouped_tile(a.rows, a.n_experts, false), a, static_cast<hipStream_t>(stream));
+  return launch_grouped<kBf16>(fp8::grouped_tile(a.rows, a.n_experts, a.n, a.nb, false), a, static_cast<hipStream_t>(stream));
 }
 
 }  // namespace qmv

@@ -117,7 +117,7 @@ void grouped() {
               if (rc != QMV_OK || rows == 0) continue;
               EXPECT(rows >= 1 && n >= 1 && e >= 1 && e <= 1024 && k % (16 / vb) == 0);
               EXPECT(stub::last.n_experts == e && stub::last.k_bytes == k * vb);
-              const int tile = fp8::grouped_tile(rows, e, kind == 0);
+              const int tile = fp8::grouped_tile(rows, e, n, fp8::blocks_of(k * vb), kind == 0);
               EXPECT(tile >= fp8::kTile32 && tile <= (kind == 0 ? fp8::kTile256 : fp8::kTile256Wide));
               EXPECT(fp8::grouped_row_tiles(rows, e, fp8::tile_rows(tile)) * fp8::ceil_div(n, fp8::tile_cols(tile)) <= fp8::kMaxTiles);
             }
