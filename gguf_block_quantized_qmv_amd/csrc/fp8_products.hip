@@ -45,17 +45,13 @@ struct Frag {
 enum Kind { kNative, kExact, kBf16 };
 constexpr bool is_e4m3(Kind kind) { return kind != kBf16; }
 
-// Sixteen e4m3 codes as two bf16 MFMA operands (exact; NaN stays NaN).
-__device__ __forceinline__ void widen(const v4i c, bf16x8 &lo, bf16x8 &hi) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)c[i], 1.0f, false);
-    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)c[i], 1.0f, true);
-    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)c[2 + i], 1.0f, false);
-    const bf16x2 e = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)c[2 + i], 1.0f, true);
-    lo[4 * i] = a[0]; lo[4 * i + 1] = a[1]; lo[4 * i + 2] = b[0]; lo[4 * i + 3] = b[1];
-    hi[4 * i] = d[0]; hi[4 * i + 1] = d[1]; hi[4 * i + 2] = e[0]; hi[4 * i + 3] = e[1];
-  }
+// Eight e4m3 codes as a bf16 MFMA operand (exact; NaN stays NaN).
+__device__ __forceinline__ bf16x8 widen(const int c0, const int c1) {
+  const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)c0, 1.0f, false);
+  const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)c0, 1.0f, true);
+  const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)c1, 1.0f, false);
+  const bf16x2 e = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8((uint32_t)c1, 1.0f, true);
+  return bf16x8{a[0], a[1], b[0], b[1], d[0], d[1], e[0], e[1]};
 }
 
 // A block's operand in the form its instructions take.
@@ -67,9 +63,14 @@ struct Operand {
 template <>
 struct Operand<kExact> {
   bf16x8 v[4];
+  // part h of the block
+  __device__ __forceinline__ void set(int h, const Frag &f) {
+    const v4i c = h < 2 ? f.lo : f.hi;
+    v[h] = h % 2 == 0 ? widen(c[0], c[1]) : widen(c[2], c[3]);
+  }
   __device__ __forceinline__ void set(const Frag &f) {
-    widen(f.lo, v[0], v[1]);
-    widen(f.hi, v[2], v[3]);
+#pragma unroll
+    for (int h = 0; h < 4; ++h) set(h, f);
   }
 };
 template <>
@@ -554,11 +555,11 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
     auto compute = [&](auto next_too, int sent, float ws, const uint8_t *stage, const float *scale, uint8_t *next,
                        float *next_scale) {
       constexpr int kEvery = (S::kLoads + (S::TM + 1) / 2 - 1) / ((S::TM + 1) / 2);
-      auto read = [&](int lo, int more, Operand<KIND> &to) {
+      auto fragment = [&](int lo, int more) {
         Frag f;
         f.lo = *reinterpret_cast<const v4i *>(stage + lo + more);
         f.hi = *reinterpret_cast<const v4i *>(stage + (lo ^ 64) + more);
-        to.set(f);
+        return f;
       };
 #pragma unroll
       for (int i = -1; i < S::TM - 1; ++i) {
@@ -568,23 +569,54 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
         const int tile = i < 0 ? kLast : i, back = i < 0 ? kLast - 1 : i == 0 ? kLast : i - 1;
         const float before = s[then] * (i <= 0 ? ws_before : ws);
         if constexpr (FP8) s[then] = scale[(wm * S::TM + i + 1) * 16 + r];
-        read(x_at, (i + 1) * 16 * kStageRow, xf[then]);
+        const Frag x_next = fragment(x_at, (i + 1) * 16 * kStageRow);
+        if constexpr (KIND != kExact) xf[then].set(x_next);
         if constexpr (decltype(next_too)::value) {
           if (i < 0) load_scales(loads, sent, next_scale);
 #pragma unroll
           for (int l = (i + 1) * kEvery; l < (i + 2) * kEvery && l < S::kLoads; ++l) load_piece(loads, l, sent, next, false);
         }
+        if constexpr (KIND == kExact) {
+          // part by part of the block, so that four columns' sums take turns in
+          // the matrix cores; the codes read above are widened behind them, each
+          // part of the old operand being done with by then
+          Frag w_next[S::TN];
+          if (i < 0) {
 #pragma unroll
-        for (int j = 0; j < S::TN; ++j) {
-          if constexpr (FP8) {
-            d[now][j] = mma_block<KIND>(wf[j], xf[now], kZero4);
-            scaled_add(before, d[then][j], acc[back][j]);
-          } else {
-            acc[tile][j] = mma_block<KIND>(wf[j], xf[now], acc[tile][j]);
+            for (int j = 0; j < S::TN; ++j) w_next[j] = fragment(w_at, w_tile(j));
           }
-          if (i < 0) read(w_at, w_tile(j), wf[j]);
-          // keeps the fma of a result TN matrix instructions behind it
-          if (KIND == kNative) __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+#pragma unroll
+            for (int j = 0; j < S::TN; ++j)
+              d[now][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[j].v[h], xf[now].v[h], h ? d[now][j] : kZero4, 0, 0, 0);
+#pragma unroll
+            for (int j = h * S::TN / 4; j < (h + 1) * S::TN / 4; ++j) scaled_add(before, d[then][j], acc[back][j]);
+            if (h >= 2) {
+#pragma unroll
+              for (int q = 2 * h - 4; q < 2 * h - 2; ++q) {
+                xf[then].set(q, x_next);
+                if (i < 0) {
+#pragma unroll
+                  for (int j = 0; j < S::TN; ++j) wf[j].set(q, w_next[j]);
+                }
+              }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < S::TN; ++j) {
+            if constexpr (FP8) {
+              d[now][j] = mma_block<KIND>(wf[j], xf[now], kZero4);
+              scaled_add(before, d[then][j], acc[back][j]);
+            } else {
+              acc[tile][j] = mma_block<KIND>(wf[j], xf[now], acc[tile][j]);
+            }
+            if (i < 0) wf[j].set(fragment(w_at, w_tile(j)));
+            // keeps the fma of a result TN matrix instructions behind it
+            if (KIND == kNative) __builtin_amdgcn_sched_barrier(0);
+          }
         }
         __builtin_amdgcn_sched_barrier(0);
       }
