@@ -412,7 +412,9 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
   // This lane's direct loads of a tile's block: row q * 8 + lane / 8 of the
   // stage, chunk by the slot, as an offset from a scalar base: the tile's first
   // row of w, and of x unless its rows are gathered (from all of x, which the
-  // host then keeps under 4 GiB). A gathered row outside x is a row of zeros.
+  // host then keeps under 4 GiB). Rows past a tile's end lie outside the buffers
+  // and are zeros that nothing has to be read for, and so is a gathered row
+  // outside x.
   struct Loads {
     Buffer x, w;
     uint32_t from[S::kLoads];
@@ -436,18 +438,17 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
 #pragma unroll
     for (int i = 0; i < S::kLoads; ++i) {
       const int q = wave * S::kLoads + i, r = q * 8 + (lane >> 3);
-      row[i] = q < S::BM / 8 ? (t.m0 + r < t.end ? t.m0 + r : t.end - 1) - x_first
-                             : t.n0 + r - S::BM < p.n ? r - S::BM : p.n - 1 - t.n0;
+      row[i] = q < S::BM / 8 ? t.m0 + r - x_first : r - S::BM;
     }
     row[S::kLoads] = t.m0 + scale_to + lane < t.end ? t.m0 + scale_to + lane : t.end - 1;
     if (gather) {   // all index loads before the first use
       int found[S::kLoads + 1];
 #pragma unroll
       for (int i = 0; i <= S::kLoads; ++i)
-        found[i] = p.index[i == S::kLoads || wave * S::kLoads + i < S::BM / 8 ? row[i] : t.m0];
+        found[i] = p.index[i < S::kLoads && wave * S::kLoads + i >= S::BM / 8 ? t.m0 : row[i] < t.end ? row[i] : t.m0];
 #pragma unroll
       for (int i = 0; i <= S::kLoads; ++i)
-        if (i == S::kLoads || wave * S::kLoads + i < S::BM / 8) row[i] = found[i];
+        if (i == S::kLoads || wave * S::kLoads + i < S::BM / 8) row[i] = row[i] < t.end ? found[i] : -1;
     }
 #pragma unroll
     for (int i = 0; i < S::kLoads; ++i) {
@@ -507,6 +508,13 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
     else return scale3;
   };
 
+  auto stage_in = [&](int v) {
+    return v == 0 ? stage0 : v == 1 ? stage1 : S::kStages > 2 && v == 2 ? stage2 : S::kStages > 3 ? stage3 : stage0;
+  };
+  auto scale_in = [&](int v) {
+    return v == 0 ? scale0 : v == 1 ? scale1 : S::kStages > 2 && v == 2 ? scale2 : S::kStages > 3 ? scale3 : scale0;
+  };
+
   // fragment addresses in a stage; chunk g + 4 is 64 bytes on or back
   const int wm = wave / S::WN, wn = wave % S::WN;
   const int r = lane & 15, g = lane >> 4;
@@ -520,6 +528,26 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
   Loads loads = loads_of(t);
   issue_first(loads, t);
   for (;;) {
+    // A wave whose rows all lie behind the tile's last one brings its share of
+    // the stages and multiplies nothing: the matrix cores of its SIMD are the
+    // other wave's (65536 rows over 128 experts, n 2048, k 768: 193 us, 189).
+    if (GROUPED && S::WM > 1 && t.m0 + wm * S::TM * 16 >= t.end) {
+      for (int b = t.blk0; b < t.blk1; ++b) {
+        if (b + kAhead < t.blk1) {
+          stage_barrier<kAfter>();
+          issue(loads, b + kAhead, stage_in((b + kAhead - t.blk0) % S::kStages), scale_in((b + kAhead - t.blk0) % S::kStages));
+        } else {
+          stage_barrier<0>();
+        }
+      }
+      at += stride;
+      stage_barrier<63>();
+      if (at >= all_count) return;
+      t = locate(id_of(at));
+      loads = loads_of(t);
+      issue_first(loads, t);
+      continue;
+    }
     const int col0 = t.n0 + wn * S::TN * 16;
     // the scale of this wave's columns, read a block ahead (a vector load: a scalar
     // one would make every wait for an LDS read of its block a full one)
