@@ -27,7 +27,7 @@ void set_error_detail(const char *what, int hip_code, const char *hip_text) {
 
 namespace {
 
-constexpr int kVersion = 10000 * 0 + 100 * 3 + 0;  // 0.3.0
+constexpr int kVersion = 10000 * 0 + 100 * 4 + 0;  // 0.4.0
 
 // a*b*c with overflow detection.
 bool mul_size(size_t a, size_t b, size_t *out) {

@@ -105,8 +105,8 @@ int qmm_fp8(const void *w, size_t w_bytes, const float *w_scale, const void *x, 
  *                within [0, rows]. An expert may have no row.
  *   row_index    int32 [rows] or NULL: row r of y takes row row_index[r] of x
  *                (a token's row may serve several experts); an index outside
- *                [0, x_rows) gives a row of zeros. NULL: row r of x, and x_rows
- *                must equal rows.
+ *                [0, x_rows) stands for a row of zeros. NULL: row r of x, and
+ *                x_rows must equal rows.
  *   y            [rows][n] of y_type, 16-byte aligned; rows in no run (before
  *                offsets[0], from offsets[n_experts] on) are left as they were
  *   rows >= 0 (0: nothing is done), n, k as in qmm_fp8, 1 <= n_experts <= QMM_MAX_EXPERTS;
