@@ -543,10 +543,12 @@ def _quant(fn, name, x, gated, xq, xs, stream):
         if k % 2:
             raise ValueError(f"{name}: x must be [m, 2 k], got {(m, k)}")
         k //= 2
-    if xq is None:
-        xq = torch.empty((m, k), dtype=torch.float8_e4m3fn, device=x.device)
-    if xs is None:
-        xs = torch.empty((_blocks(k), m), dtype=torch.float32, device=x.device)
+    if xq is None or xs is None:
+        with torch.cuda.stream(stream):   # memory of the stream that writes it
+            if xq is None:
+                xq = torch.empty((m, k), dtype=torch.float8_e4m3fn, device=x.device)
+            if xs is None:
+                xs = torch.empty((_blocks(k), m), dtype=torch.float32, device=x.device)
     xp = _take(x, "x", _FLOATS, x.shape, index)
     _run(fn, name, index, stream, xp, _FLOATS[x.dtype], _take(xq, "xq", _E4M3, (m, k), index),
          _take(xs, "xs", _F32, (_blocks(k), m), index), m, k)
@@ -586,7 +588,8 @@ def qmm_fp8(w, w_scale, x, x_scale, n: int, k: int, y=None, out_dtype=None, ws=N
     torch = _torch()
     index, (m, _) = _first(x, "x", _E4M3, 2)
     if y is None:
-        y = torch.empty((m, n), dtype=out_dtype or torch.float32, device=x.device)
+        with torch.cuda.stream(stream):   # memory of the stream that writes it
+            y = torch.empty((m, n), dtype=out_dtype or torch.float32, device=x.device)
     y_type = _y_type(y, out_dtype)
     if ws is None:
         need = lib.qmm_fp8_workspace(m, n, k, y_type)

@@ -94,10 +94,10 @@ def grouped(x, w, offsets, y, index=None):
     y = np.array(y, dtype=np.float64)
     mag = np.zeros_like(y)
     for e, we in enumerate(w):
-        for r in range(offsets[e], offsets[e + 1]):
-            src = r if index is None else index[r]
-            if 0 <= src < len(x):
-                y[r], mag[r] = (v[0] for v in product(x[src:src + 1], we))
-            else:
-                y[r], mag[r] = 0.0, 0.0
+        run = np.arange(offsets[e], offsets[e + 1])
+        src = run if index is None else np.asarray(index)[run]
+        inside = (src >= 0) & (src < len(x))
+        y[run], mag[run] = 0.0, 0.0
+        if inside.any():
+            y[run[inside]], mag[run[inside]] = product(x[src[inside]], we)
     return y, mag

@@ -262,6 +262,25 @@ def test_grouped(q, dev, kind, out, counts, n, k, x_rows, gather, lead, spare):
     assert (host(y.float())[outside] == -7.0).all()
 
 
+# the largest tiles, several to a workgroup: runs that end in a tile's first rows, in its first half, at its end
+LONG_RUNS = [1, 1024, 257, 0, 300, 1153, 255, 128, 769, 511, 16, 1409]
+
+
+@pytest.mark.parametrize("out", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["fp8", "bf16"])
+@pytest.mark.parametrize("n,k,gather", [(1500, 400, True), (1288, 1040, False)])
+def test_grouped_long_runs(q, dev, kind, out, n, k, gather):
+    off, index, data, w, x = grouped_case(4, kind, LONG_RUNS, n, k, 900, gather, 3, 5)
+    y, buf = guarded((8 + sum(LONG_RUNS), n), out, dev)
+    y.fill_(-7.0)
+    run_grouped(q, dev, kind, off, index, data, n, k, y)
+    torch.cuda.synchronize()
+    assert guards_intact(buf)
+    exact, mag = o.grouped(x, w, off, np.full(y.shape, -7.0), index)
+    check(host(y.double()), exact, bound(mag, k, out, exact, kind == "bf16"))
+    assert (host(y.float())[[0, 1, 2, -5, -4, -3, -2, -1]] == -7.0).all()
+
+
 @pytest.mark.parametrize("kind", ["fp8", "bf16"])
 @pytest.mark.parametrize("counts", [[2, 0, 3], [40, 0, 60]])
 def test_grouped_indices_outside_x_give_zeros(q, dev, kind, counts):
