@@ -211,6 +211,20 @@ def test_dense_values_that_are_not_finite_stay_in_their_row_and_column(q, dev, m
     assert np.array_equal(y[keep], clean[keep])
 
 
+@pytest.mark.parametrize("m,n", [(2, 150), (40, 150), (100, 300), (700, 1400), (2100, 4200)])
+def test_dense_bf16_values_that_are_not_finite_stay_in_their_row_and_column(q, dev, m, n):
+    k = 400
+    w, ws, x, xs = dense_case(3, m, n, k)
+    clean = host(q.qmm_fp8(up(w, dev), up(ws, dev), up(x, dev), up(xs, dev), n, k, out_dtype=torch.bfloat16).float())
+    assert np.isfinite(clean).all()
+    x[1, 399], w[n - 1, 3], xs[2, 0] = 0x7F, 0xFF, np.inf
+    y = host(q.qmm_fp8(up(w, dev), up(ws, dev), up(x, dev), up(xs, dev), n, k, out_dtype=torch.bfloat16).float())
+    assert np.isnan(y[1]).all() and np.isnan(y[:, n - 1]).all() and not np.isfinite(y[0]).any()
+    keep = np.ones((m, n), bool)
+    keep[:2], keep[:, n - 1] = False, False
+    assert np.array_equal(y[keep], clean[keep])
+
+
 # ------------------------------------------------------------------ grouped
 
 def grouped_case(seed, kind, counts, n, k, x_rows, gather, lead=0, spare=0):
@@ -271,6 +285,9 @@ LONG_RUNS = [1, 1024, 257, 0, 300, 1153, 255, 128, 769, 511, 16, 1409]
 @pytest.mark.parametrize("n,k,gather", [(1500, 400, True), (1288, 1040, False)])
 def test_grouped_long_runs(q, dev, kind, out, n, k, gather):
     off, index, data, w, x = grouped_case(4, kind, LONG_RUNS, n, k, 900, gather, 3, 5)
+    if gather:
+        index[::97] = -1                                     # rows of zeros
+        index[50::97] = 900
     y, buf = guarded((8 + sum(LONG_RUNS), n), out, dev)
     y.fill_(-7.0)
     run_grouped(q, dev, kind, off, index, data, n, k, y)
