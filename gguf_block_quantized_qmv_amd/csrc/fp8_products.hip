@@ -747,13 +747,12 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
     // 32 (from two tiles), or 4 g .. 4 g + 3 of each 16.
     constexpr int kWide = S::kPairs ? 8 : 4;
     if (!GROUPED && done.part >= 0) {
-      float *to = p.part + (size_t)done.part * (S::BM * S::BN);
+      // a part keeps the order of the registers: 1 KiB a store, in one piece
+      float *to = p.part + (size_t)done.part * (S::BM * S::BN) + (size_t)wave * (S::TM * S::TN * 256) + lane * 4;
 #pragma unroll
       for (int i = 0; i < S::TM; ++i)
 #pragma unroll
-        for (int j = 0; j < S::TN; ++j)
-          *reinterpret_cast<v4f *>(to + ((wm * S::TM + i) * 16 + r) * S::BN + wn * S::TN * 16 +
-                                   (S::kPairs ? j / 2 * 32 + g * 8 + j % 2 * 4 : j * 16 + g * 4)) = acc[i][j];
+        for (int j = 0; j < S::TN; ++j) *reinterpret_cast<v4f *>(to + (i * S::TN + j) * 256) = acc[i][j];
       if (!more) return;
       continue;
     }
@@ -798,30 +797,50 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
   }
 }
 
-// y of the tiles that were cut along k: the parts in the order of k, four
-// columns a thread.
+// y of the tiles that were cut along k: the parts in the order of k, a lane's
+// four or eight neighbouring columns a thread.
 template <class S>
 __global__ __launch_bounds__(256) void product_sum_kernel(const ProductArgs p, const int t_main, const int r_tiles,
                                                           const int splits) {
-  constexpr int kQuads = S::BM * S::BN / 4;
-  const int in = ((int)blockIdx.x * 256 + (int)threadIdx.x) % kQuads;
-  const int tile = uniform(((int)blockIdx.x * 256 + (int)threadIdx.x) / kQuads);   // whole blocks to a tile
+  constexpr int kQuads = S::kPairs ? 2 : 1, kWide = 4 * kQuads, kRow = S::TN / kQuads;
+  constexpr int kThreads = S::BM * S::BN / kWide;   // of a tile, whole blocks
+  const int at = (int)blockIdx.x * 256 + (int)threadIdx.x, in = at % kThreads, tile = uniform(at / kThreads);
+  const int lane = in & 63, j = in / 64 % kRow * kQuads, i = in / (64 * kRow) % S::TM, wave = in / (64 * kRow * S::TM);
   int m0, n0;
   tile_place<S>(t_main + tile, p.rows, fp8::ceil_div(p.n, S::BN), m0, n0);
-  const int row = m0 + in / (S::BN / 4), col = n0 + in % (S::BN / 4) * 4;
+  const int row = m0 + (wave / S::WN * S::TM + i) * 16 + (lane & 15);
+  const int col = n0 + (wave % S::WN * S::TN + j) * 16 + (lane >> 4) * kWide;
   if (row >= p.rows || col >= p.n) return;
-  const v4f *from = reinterpret_cast<const v4f *>(p.part) + (size_t)tile * kQuads + in;
-  v4f v = *from;
-  for (int s = 1; s < splits; ++s) v += from[(size_t)s * r_tiles * kQuads];
-  const size_t at = (size_t)row * p.n + col;
+  const float *from = p.part + (size_t)tile * (S::BM * S::BN) + ((wave * S::TM + i) * S::TN + j) * 256 + lane * 4;
+  v4f v[kQuads];
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (col + e < p.n) {
-      if (p.y_bf16)
-        static_cast<__bf16 *>(p.y)[at + e] = (__bf16)v[e];
-      else
-        static_cast<float *>(p.y)[at + e] = v[e];
-    }
+  for (int h = 0; h < kQuads; ++h) v[h] = *reinterpret_cast<const v4f *>(from + h * 256);
+  for (int s = 1; s < splits; ++s)
+#pragma unroll
+    for (int h = 0; h < kQuads; ++h)
+      v[h] += *reinterpret_cast<const v4f *>(from + (size_t)s * r_tiles * (S::BM * S::BN) + h * 256);
+  const size_t place = (size_t)row * p.n + col;
+  typedef __bf16 RowBf16 __attribute__((ext_vector_type(kWide), aligned(2)));
+  typedef float RowF32 __attribute__((ext_vector_type(4), aligned(4)));
+  if (col + kWide > p.n) {
+#pragma unroll
+    for (int e = 0; e < kWide; ++e)
+      if (col + e < p.n) {
+        if (p.y_bf16)
+          static_cast<__bf16 *>(p.y)[place + e] = (__bf16)v[e / 4][e % 4];
+        else
+          static_cast<float *>(p.y)[place + e] = v[e / 4][e % 4];
+      }
+  } else if (p.y_bf16) {
+    RowBf16 o;
+#pragma unroll
+    for (int e = 0; e < kWide; ++e) o[e] = (__bf16)v[e / 4][e % 4];
+    *reinterpret_cast<RowBf16 *>(static_cast<__bf16 *>(p.y) + place) = o;
+  } else {
+#pragma unroll
+    for (int h = 0; h < kQuads; ++h)
+      *reinterpret_cast<RowF32 *>(static_cast<float *>(p.y) + place + h * 4) = RowF32{v[h][0], v[h][1], v[h][2], v[h][3]};
+  }
 }
 
 using Tile32 = Shape<32, 64, 1, 4, 3>;
@@ -842,7 +861,7 @@ int launch_dense(const ProductArgs &a, const fp8::DensePlan &plan, hipStream_t s
                                dim3(grid_of<S>((int64_t)plan.t_main + (int64_t)plan.r_tiles * plan.splits)),
                                dim3(S::kThreads), 0, s, a, plan.t_main, plan.r_tiles, plan.splits);
   if (rc || plan.r_tiles == 0) return rc;
-  return launch_kernel("product_sum_kernel", product_sum_kernel<S>, dim3((unsigned)(plan.r_tiles * (S::BM * S::BN / 1024))),
+  return launch_kernel("product_sum_kernel", product_sum_kernel<S>, dim3((unsigned)(plan.r_tiles * (S::BM * S::BN / (S::kPairs ? 2048 : 1024)))),
                        dim3(256), 0, s, a, plan.t_main, plan.r_tiles, plan.splits);
 }
 
