@@ -266,7 +266,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
 //
 // What bounds it, and why these shapes:
 //  * Long products: the matrix cores and their power. 4096 x 17408 x 5120 in
-//    bf16 takes 340 us, 2.15 PFLOP/s; the same call on zeros takes a fifth
+//    bf16 takes 335 us, 2.18 PFLOP/s; the same call on zeros takes a fifth
 //    less. Of the shapes only 256 x 256 (waves of 128 x 64) asks LDS for no
 //    more than it gives beside the matrix instructions; a step of it takes 1.8
 //    us, two of 256 x 128 (waves of 64 x 64) take 2.3. Its sums fill the
@@ -274,7 +274,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
 //  * fp32 results: 700 us, 1.04 PFLOP/s; two conversions for each bf16 matrix
 //    instruction share the issue slots with the fma.
 //  * Few steps a tile (k of 768): the stores. 65536 rows over 128 experts, n
-//    2048: 189 us, of which 50 are the 268 MB of y at the card's write rate;
+//    2048: 187 to 196 us, of which 50 are the 268 MB of y at the card's write rate;
 //    the loads of a following tile beyond its first blocks queue behind them.
 //    Smaller tiles, two workgroups a CU, overlap them and lose more to LDS
 //    (128 x 128: 224 us).
