@@ -188,6 +188,24 @@ def test_dense_large_tiles(q, dev, out, m, n, k):
     assert torch.equal(q.qmm_fp8(*args, out_dtype=out), y)
 
 
+@pytest.mark.parametrize("m,n,k,out", [
+    (17, 6514, 2576, "bf16"), (33, 6475, 1728, "f32"), (386, 8255, 2448, "f32"), (129, 5377, 4400, "f32"),
+    (129, 5406, 5664, "bf16"), (1027, 7211, 912, "f32"), (385, 8327, 5648, "bf16"), (2049, 7245, 912, "bf16")])
+def test_dense_tiles_cut_along_k(q, dev, m, n, k, out):
+    # every tile shape with parts, alone and behind whole tiles; odd rows of y, a last row tile of one row
+    out = torch.float32 if out == "f32" else torch.bfloat16
+    assert q.qmm_fp8_workspace(m, n, k, out) > 0
+    w, ws, x, xs = dense_case(13, m, n, k)
+    y, buf = guarded((m, n), out, dev)
+    need = q.qmm_fp8_workspace(m, n, k, out)
+    space = torch.full((need + 256,), 0xFF, dtype=torch.uint8, device=dev)
+    q.qmm_fp8(up(w, dev), up(ws, dev), up(x, dev), up(xs, dev), n, k, y=y, ws=space[:need])
+    torch.cuda.synchronize()
+    assert guards_intact(buf) and bool((space[need:] == 0xFF).all())
+    exact, mag = o.product(o.rows_f64(x, xs), o.weights_f64(w, ws))
+    check(host(y.double()), exact, bound(mag, k, out, exact))
+
+
 @pytest.mark.parametrize("n,k", [(130, 256), (100, 2064), (48, 8192), (6004, 528), (4100, 9216)])
 def test_dense_rows_have_the_same_bits_in_any_company(q, dev, n, k):
     w, ws, x, xs = dense_case(2, 16, n, k)
