@@ -124,23 +124,24 @@ inline StreamPlan stream_plan(int m, int n, int nb) {
 
 // Host code cannot see the offsets: rows are taken as spread evenly, half a
 // tile lost at the end of each expert's run. Of the tiles the one with the
-// least time by this model, in ns: a step of one block of k takes 800 (32 x 64,
-// four workgroups a CU), 900 (64 x 128, two), 750 (128 x 128), 1150 (256 x 128)
-// and 1800 (256 x 256), in fp32 results of e4m3 up to twice that; a tile starts
-// and ends in 6000.
+// least time by this model, in ns: a step of one block of k takes 700 (32 x 64,
+// four workgroups a CU), 900 (64 x 128, two), 750 (128 x 128) and 1800 (256 x
+// 256), in fp32 results of e4m3 900, 1200 and 2200 (256 x 128); a tile starts
+// and ends in 6000. (8 rows, 8 of 128 experts of 1536 x 2048: 8.5 us by 32 x 64,
+// 11.4 by 64 x 128, 10.1 by 128 x 128; 4096 rows: 102, 84, 88.)
 inline int grouped_tile(int rows, int n_experts, int n, int nb, bool exact) {
   const int busy = rows < n_experts ? rows : n_experts;
   int best = kTile32;
   int64_t least = INT64_MAX;
   for (int tile = kTile32; tile <= (exact ? kTile256 : kTile256Wide); ++tile) {
-    if (tile == kTile256 && !exact) continue;   // 256 x 256 does better
+    if (tile == (exact ? kTile128 : kTile256)) continue;   // 64 x 128 and 256 x 256 do better
     const int bm = tile_rows(tile), per_cu = tile == kTile32 ? 4 : tile == kTile64 ? 2 : 1;
     int64_t row_tiles = ((int64_t)rows + (int64_t)busy * bm / 2) / bm;
     if (row_tiles < busy) row_tiles = busy;
     const int64_t tiles = row_tiles * ceil_div(n, tile_cols(tile));
     const int64_t rounds = (tiles + per_cu * kSlots - 1) / (per_cu * kSlots);
-    const int64_t step = tile == kTile32 ? (exact ? 900 : 800) : tile == kTile64 ? (exact ? 1200 : 900)
-                         : tile == kTile128 ? (exact ? 1300 : 750) : tile == kTile256 ? 2200 : 1800;
+    const int64_t step = tile == kTile32 ? (exact ? 900 : 700) : tile == kTile64 ? (exact ? 1200 : 900)
+                         : tile == kTile128 ? 750 : tile == kTile256 ? 2200 : 1800;
     const int64_t cost = rounds * (nb * step + 6000);
     if (cost < least) {
       least = cost;

@@ -878,12 +878,12 @@ int launch_grouped(const ProductArgs &a, hipStream_t s) {
 
 template <Kind KIND>
 int launch_grouped(int tile, const ProductArgs &a, hipStream_t s) {
-  switch (tile) {
-    case fp8::kTile32: return launch_grouped<Tile32, KIND>(a, s);
-    case fp8::kTile64: return launch_grouped<Tile64, KIND>(a, s);
-    case fp8::kTile128: return launch_grouped<Tile128, KIND>(a, s);
-    case fp8::kTile256: return launch_grouped<Tile256, kExact>(a, s);         // fp32 results of e4m3
-    default: return launch_grouped<Tile256Wide, KIND == kBf16 ? kBf16 : kNative>(a, s);
+  if (tile == fp8::kTile32) return launch_grouped<Tile32, KIND>(a, s);
+  if (tile == fp8::kTile64) return launch_grouped<Tile64, KIND>(a, s);
+  if constexpr (KIND == kExact) {
+    return launch_grouped<Tile256, KIND>(a, s);
+  } else {
+    return tile == fp8::kTile128 ? launch_grouped<Tile128, KIND>(a, s) : launch_grouped<Tile256Wide, KIND>(a, s);
   }
 }
 

@@ -294,19 +294,22 @@ def test_grouped(q, dev, kind, out, counts, n, k, x_rows, gather, lead, spare):
     assert (host(y.float())[outside] == -7.0).all()
 
 
-# the largest tiles, several to a workgroup: runs that end in a tile's first rows, in its first half, at its end
+# the larger tiles, several to a workgroup: runs that end in a tile's first rows, in its first half, at its end
 LONG_RUNS = [1, 1024, 257, 0, 300, 1153, 255, 128, 769, 511, 16, 1409]
 
 
 @pytest.mark.parametrize("out", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("kind", ["fp8", "bf16"])
-@pytest.mark.parametrize("n,k,gather", [(1500, 400, True), (1288, 1040, False)])
-def test_grouped_long_runs(q, dev, kind, out, n, k, gather):
-    off, index, data, w, x = grouped_case(4, kind, LONG_RUNS, n, k, 900, gather, 3, 5)
+@pytest.mark.parametrize("runs,n,k,gather", [
+    (LONG_RUNS, 1500, 400, True), (LONG_RUNS, 1288, 1040, False),
+    ([700, 65, 1153, 0, 130, 893], 647, 1040, True), ([40, 77, 0, 64, 65, 1] * 9 + [600], 514, 656, False)],
+    ids=["256", "256-deep", "128", "64"])
+def test_grouped_long_runs(q, dev, kind, out, runs, n, k, gather):
+    off, index, data, w, x = grouped_case(4, kind, runs, n, k, 900, gather, 3, 5)
     if gather:
         index[::97] = -1                                     # rows of zeros
         index[50::97] = 900
-    y, buf = guarded((8 + sum(LONG_RUNS), n), out, dev)
+    y, buf = guarded((8 + sum(runs), n), out, dev)
     y.fill_(-7.0)
     run_grouped(q, dev, kind, off, index, data, n, k, y)
     torch.cuda.synchronize()
