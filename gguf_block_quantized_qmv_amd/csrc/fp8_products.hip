@@ -266,7 +266,7 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
 //
 // What bounds it, and why these shapes:
 //  * Long products: the matrix cores and their power. 4096 x 17408 x 5120 in
-//    bf16 takes 335 us, 2.18 PFLOP/s; the same call on zeros takes a fifth
+//    bf16 takes 322 to 338 us, 2.2 PFLOP/s; the same call on zeros takes a fifth
 //    less. Of the shapes only 256 x 256 (waves of 128 x 64) asks LDS for no
 //    more than it gives beside the matrix instructions; a step of it takes 1.8
 //    us, two of 256 x 128 (waves of 64 x 64) take 2.3. Its sums fill the
