@@ -487,6 +487,7 @@ _U8 = (_torch().uint8,)
 _E4M3 = (_torch().float8_e4m3fn, _torch().uint8)
 _BF16 = _bf16_types()
 _FLOATS = {_torch().float32: 0, _torch().bfloat16: 1}   # QMM_F32, QMM_BF16
+_FAST_SUMS = 16                                         # QMM_FAST_SUMS
 
 
 def _explain(t, name, types, shape, index):
@@ -565,32 +566,44 @@ def qmm_fp8_quant_silu_mul(x, xq=None, xs=None, stream=None):
     return _quant(lib.qmm_fp8_quant_silu_mul, "qmm_fp8_quant_silu_mul", x, True, xq, xs, stream)
 
 
-def qmm_fp8_workspace(m: int, n: int, k: int, out_dtype=None) -> int:
+def _type_code(dtype, fast_sums):
+    code = _FLOATS[dtype]
+    if not fast_sums:
+        return code
+    if code != 1:
+        raise ValueError("fast_sums goes with a bfloat16 result")
+    return code | _FAST_SUMS
+
+
+def qmm_fp8_workspace(m: int, n: int, k: int, out_dtype=None, fast_sums: bool = False) -> int:
     """Bytes of ws a qmm_fp8 call of this shape needs (y fp32 unless out_dtype says bf16)."""
-    return lib.qmm_fp8_workspace(m, n, k, 0 if out_dtype is None else _FLOATS[out_dtype])
+    return lib.qmm_fp8_workspace(m, n, k, 0 if out_dtype is None else _type_code(out_dtype, fast_sums))
 
 
-def _y_type(y, out_dtype):
+def _y_type(y, out_dtype, fast_sums=False):
     if y.dtype not in _FLOATS:
         raise TypeError(f"y has dtype {y.dtype}, expected float32 or bfloat16")
     if out_dtype is not None and y.dtype != out_dtype:
         raise TypeError(f"y has dtype {y.dtype}, out_dtype is {out_dtype}")
-    return _FLOATS[y.dtype]
+    return _type_code(y.dtype, fast_sums)
 
 
-def qmm_fp8(w, w_scale, x, x_scale, n: int, k: int, y=None, out_dtype=None, ws=None, stream=None):
+def qmm_fp8(w, w_scale, x, x_scale, n: int, k: int, y=None, out_dtype=None, ws=None, stream=None,
+            fast_sums: bool = False):
     """y[m, n] = x @ w^T for e4m3 w [n, k] and x [m, k] with scales w_scale [ceil(n/128), ceil(k/128)] and
     x_scale [ceil(k/128), m] (as qmm_fp8_quant gives them); y is fp32 unless y or out_dtype says bf16.
 
     ws: None allocates the workspace the shape needs (if any), or a uint8 device
-    tensor of at least qmm_fp8_workspace(m, n, k, y.dtype) bytes to reuse.
+    tensor of at least qmm_fp8_workspace(m, n, k, y.dtype, fast_sums) bytes to reuse.
+    fast_sums (bf16 y): the e4m3 matrix instruction, twice the rate for many rows,
+    which cuts partial sums (QMM_FAST_SUMS in qmm_fp8.h).
     """
     torch = _torch()
     index, (m, _) = _first(x, "x", _E4M3, 2)
     if y is None:
         with torch.cuda.stream(stream):   # memory of the stream that writes it
             y = torch.empty((m, n), dtype=out_dtype or torch.float32, device=x.device)
-    y_type = _y_type(y, out_dtype)
+    y_type = _y_type(y, out_dtype, fast_sums)
     if ws is None:
         need = lib.qmm_fp8_workspace(m, n, k, y_type)
         if need:
@@ -604,7 +617,7 @@ def qmm_fp8(w, w_scale, x, x_scale, n: int, k: int, y=None, out_dtype=None, ws=N
     return y
 
 
-def _grouped(fn, name, types, w, w_scale, x, x_scale, offsets, n, k, row_index, y, out_dtype, stream):
+def _grouped(fn, name, types, w, w_scale, x, x_scale, offsets, n, k, row_index, y, out_dtype, stream, fast_sums=False):
     torch = _torch()
     index, (x_rows, _) = _first(x, "x", types, 2)
     _, (e, _, _) = _first(w, "w", types, 3)
@@ -617,7 +630,7 @@ def _grouped(fn, name, types, w, w_scale, x, x_scale, offsets, n, k, row_index, 
         # rows that belong to no expert are not written: zeros there rather than what the memory held
         with torch.cuda.stream(stream):
             y = torch.zeros((rows, n), dtype=out_dtype or torch.float32, device=x.device)
-    y_type = _y_type(y, out_dtype)
+    y_type = _y_type(y, out_dtype, fast_sums)
     wp, xp = _take(w, "w", types, (e, n, k), index), _take(x, "x", types, (x_rows, k), index)
     op, yp = _take(offsets, "offsets", _I32, (e + 1,), index), _take(y, "y", _FLOATS, (rows, n), index)
     if types is _E4M3:
@@ -631,15 +644,15 @@ def _grouped(fn, name, types, w, w_scale, x, x_scale, offsets, n, k, row_index, 
 
 
 def qmm_fp8_grouped(w, w_scale, x, x_scale, offsets, n: int, k: int, row_index=None, y=None, out_dtype=None,
-                    stream=None):
+                    stream=None, fast_sums: bool = False):
     """Rows offsets[e] .. offsets[e+1] - 1 of y [rows, n] = x rows @ w[e]^T for e4m3 w [experts, n, k] and x, scales as
     in qmm_fp8 with one more leading dimension for w_scale; offsets int32 [experts + 1] on the device.
 
     row_index (int32, one per row of y): the row of x to take, outside x for a row of zeros; None: the same row.
-    Rows of y that belong to no expert are left as they were (zeros when y is None).
+    Rows of y that belong to no expert are left as they were (zeros when y is None). fast_sums as in qmm_fp8.
     """
     return _grouped(lib.qmm_fp8_grouped, "qmm_fp8_grouped", _E4M3, w, w_scale, x, x_scale, offsets, n, k, row_index, y,
-                    out_dtype, stream)
+                    out_dtype, stream, fast_sums)
 
 
 def qmm_bf16_grouped(w, x, offsets, n: int, k: int, row_index=None, y=None, out_dtype=None, stream=None):

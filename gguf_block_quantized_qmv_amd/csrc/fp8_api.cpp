@@ -22,6 +22,14 @@ bool overlap(const void *p, size_t pb, const void *q, size_t qb) {
 bool type_ok(int t) { return t == QMM_F32 || t == QMM_BF16; }
 size_t type_bytes(int t) { return t == QMM_F32 ? 4 : 2; }
 
+// Takes QMM_FAST_SUMS off the y_type of an e4m3 product; what is left of a
+// value it cannot stand with is no type.
+bool take_fast(int *y_type) {
+  if (*y_type != (QMM_BF16 | QMM_FAST_SUMS)) return false;
+  *y_type = QMM_BF16;
+  return true;
+}
+
 // k: a positive multiple of `step`, within range. n likewise without the step.
 int check_nk(int n, int k, int step) {
   if (n < 1 || k < step || k % step) return QMV_ERR_SHAPE;
@@ -47,7 +55,7 @@ int quant(const void *x, int x_type, bool gated, uint8_t *xq, float *xs, int m, 
 int grouped(const void *w, size_t w_bytes, const float *w_scale, const void *x, const float *x_scale,
             const int32_t *offsets, const int32_t *row_index, void *y, int y_type, int rows, int x_rows, int n, int k,
             int n_experts, int value_bytes, void *stream) {
-  const bool e4m3 = value_bytes == 1;
+  const bool e4m3 = value_bytes == 1, fast = e4m3 && take_fast(&y_type), exact = e4m3 && !fast;
   if (!type_ok(y_type)) return QMV_ERR_RANGE;
   if (rows < 0 || rows > QMM_MAX_ROWS || x_rows < 0 || x_rows > QMM_MAX_ROWS || n_experts < 1 ||
       n_experts > QMM_MAX_EXPERTS)
@@ -59,7 +67,7 @@ int grouped(const void *w, size_t w_bytes, const float *w_scale, const void *x, 
   const size_t wb = (size_t)n_experts * n * k * value_bytes;   // <= 2^51
   if (w_bytes != wb) return QMV_ERR_SIZE;
   if (rows == 0) return QMV_OK;
-  if (!qmv::fp8::grouped_in_grid(rows, n_experts, n, qmv::fp8::blocks_of(k * value_bytes), e4m3 && y_type == QMM_F32)) return QMV_ERR_RANGE;
+  if (!qmv::fp8::grouped_in_grid(rows, n_experts, n, qmv::fp8::blocks_of(k * value_bytes), exact)) return QMV_ERR_RANGE;
   // rows are gathered by 32-bit byte offsets
   if (row_index && (size_t)x_rows * k * value_bytes > UINT32_MAX) return QMV_ERR_RANGE;
   // with no row of x every index is out of range, and x itself may be null
@@ -90,6 +98,7 @@ int grouped(const void *w, size_t w_bytes, const float *w_scale, const void *x, 
   a.nb = qmv::fp8::blocks_of(a.k_bytes);
   a.n_experts = n_experts;
   a.y_bf16 = y_type == QMM_BF16;
+  a.fast = fast;
   return e4m3 ? qmv::launch_fp8_grouped(a, stream) : qmv::launch_bf16_grouped(a, stream);
 }
 
@@ -110,13 +119,15 @@ int qmm_fp8_quant_silu_mul(const void *x, int x_type, uint8_t *xq, float *xs, in
 }
 
 size_t qmm_fp8_workspace(int m, int n, int k, int y_type) {
+  const bool fast = take_fast(&y_type);
   if (!type_ok(y_type) || !dense_in_range(m, n, k)) return 0;
-  return qmv::fp8::dense_workspace(m, n, k, y_type == QMM_BF16);
+  return qmv::fp8::dense_workspace(m, n, k, fast);
 }
 
 int qmm_fp8(const void *w, size_t w_bytes, const float *w_scale, const void *x, const float *x_scale, void *y,
             int y_type, int m, int n, int k, void *ws, size_t ws_bytes, void *stream) {
   if (!w || !w_scale || !x || !x_scale || !y) return QMV_ERR_NULL;
+  const bool fast = take_fast(&y_type);
   if (!type_ok(y_type)) return QMV_ERR_RANGE;
   if (m < 1 || m > QMM_MAX_ROWS) return QMV_ERR_RANGE;
   const int rc = check_nk(n, k, 16);
@@ -128,7 +139,7 @@ int qmm_fp8(const void *w, size_t w_bytes, const float *w_scale, const void *x, 
       !aligned(ws, 256))
     return QMV_ERR_ALIGN;
   const size_t nb = (size_t)qmv::fp8::blocks_of(k);
-  const size_t yb = (size_t)m * n * type_bytes(y_type), need = qmv::fp8::dense_workspace(m, n, k, y_type == QMM_BF16);
+  const size_t yb = (size_t)m * n * type_bytes(y_type), need = qmv::fp8::dense_workspace(m, n, k, fast);
   const void *in_p[] = {w, w_scale, x, x_scale};
   const size_t in_b[] = {wb, (size_t)qmv::fp8::blocks_of(n) * nb * 4, (size_t)m * k, (size_t)m * nb * 4};
   for (int i = 0; i < 4; ++i)
@@ -153,6 +164,7 @@ int qmm_fp8(const void *w, size_t w_bytes, const float *w_scale, const void *x, 
   a.nb = qmv::fp8::blocks_of(k);
   a.n_experts = 1;
   a.y_bf16 = y_type == QMM_BF16;
+  a.fast = fast;
   return qmv::launch_fp8_dense(a, stream);
 }
 

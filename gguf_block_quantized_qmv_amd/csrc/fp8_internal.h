@@ -20,6 +20,7 @@ struct ProductArgs {
   void *y;
   float *part;             // the workspace of a dense plan with parts
   int rows, x_rows, n, k_bytes, nb, n_experts, y_bf16;
+  int fast;                // e4m3: QMM_FAST_SUMS
 };
 
 int launch_fp8_quant(const void *x, bool x_f32, bool gated, uint8_t *xq, float *xs, int m, int k, void *stream);

@@ -64,20 +64,21 @@ inline size_t split_bytes(const DensePlan &p) {
   return p.splits > 1 ? (size_t)p.r_tiles * p.splits * tile_rows(p.tile) * tile_cols(p.tile) * 4 : 0;
 }
 
-inline DensePlan dense_plan(int m, int n, int k, bool y_bf16) {
+// fast: QMM_FAST_SUMS is asked for.
+inline DensePlan dense_plan(int m, int n, int k, bool fast) {
   const int nb = blocks_of(k);
   if (m <= QMM_SAME_ROWS || (m <= kStreamRows && (int64_t)n * k * ceil_div(m, 16) < kStreamBytes))
     return DensePlan{true, kTile32, 0, 0, 1};
   if (m <= 128) return split_plan(m <= 32 ? kTile32 : m <= 64 ? kTile64 : kTile128, m, n, nb);
   // Of the large tiles the one with the least time by this model, in ns: a step
-  // of one block of k takes, with every CU at work, 1800 (256 x 256), 1150
-  // (256 x 128) and 750 (128 x 128), in fp32 results 2200 and 1300; a tile
+  // of one block of k takes, with every CU at work, 2200 (256 x 128) and 1300
+  // (128 x 128), with fast sums 1150, 750 and 1800 (256 x 256); a tile
   // starts and ends in 8000; parts are written and read at 5 bytes a ps.
   DensePlan best{};
   int64_t least = INT64_MAX;
-  for (int tile = kTile128; tile <= (y_bf16 ? kTile256Wide : kTile256); ++tile) {
+  for (int tile = kTile128; tile <= (fast ? kTile256Wide : kTile256); ++tile) {
     const DensePlan p = split_plan(tile, m, n, nb);
-    const int64_t step = tile == kTile256Wide ? 1800 : tile == kTile256 ? (y_bf16 ? 1150 : 2200) : y_bf16 ? 750 : 1300;
+    const int64_t step = tile == kTile256Wide ? 1800 : tile == kTile256 ? (fast ? 1150 : 2200) : fast ? 750 : 1300;
     const int64_t rounds = (p.t_main + kSlots - 1) / kSlots;
     int64_t cost = rounds * (nb * step + 8000);
     if (p.r_tiles) cost += ceil_div(nb, p.splits) * step + 8000 + 3000 + (int64_t)split_bytes(p) * 2 / 5000;
@@ -89,7 +90,7 @@ inline DensePlan dense_plan(int m, int n, int k, bool y_bf16) {
   return best;
 }
 
-inline size_t dense_workspace(int m, int n, int k, bool y_bf16) { return split_bytes(dense_plan(m, n, k, y_bf16)); }
+inline size_t dense_workspace(int m, int n, int k, bool fast) { return split_bytes(dense_plan(m, n, k, fast)); }
 
 // The streaming kernel: `tile` weight rows (a multiple of four, so that a
 // lane's four results lie under one scale; above 16, two fragments a wave) and
@@ -126,8 +127,8 @@ inline StreamPlan stream_plan(int m, int n, int nb) {
 // tile lost at the end of each expert's run. Of the tiles the one with the
 // least time by this model, in ns: a step of one block of k takes 700 (32 x 64,
 // four workgroups a CU), 900 (64 x 128, two), 750 (128 x 128) and 1800 (256 x
-// 256), in fp32 results of e4m3 900, 1200 and 2200 (256 x 128); a tile starts
-// and ends in 6000. (8 rows, 8 of 128 experts of 1536 x 2048: 8.5 us by 32 x 64,
+// 256), for codes widened to bf16 (`exact`: e4m3 without fast sums) 900, 1200
+// and 2200 (256 x 128); a tile starts and ends in 6000. (8 rows, 8 of 128 experts of 1536 x 2048: 8.5 us by 32 x 64,
 // 11.4 by 64 x 128, 10.1 by 128 x 128; 4096 rows: 102, 84, 88.)
 inline int grouped_tile(int rows, int n_experts, int n, int nb, bool exact) {
   const int busy = rows < n_experts ? rows : n_experts;

@@ -11,19 +11,21 @@
 // e4m3: the scales vary from block to block, so a block's product starts from
 // zero and enters the sum by one fma per result, y += (xs * ws) * d, in fp32.
 // Two ways to a block's product:
-//  * kNative, one v_mfma_f32_16x16x128_f8f6f4. The instruction aligns each
-//    eight neighbouring products to the largest of them and cuts what lies 13
-//    bits below (measured: 2^16 + 2^2 in one group of eight gives 2^16, in two
-//    groups 2^16 + 2^2); on normal data that is 1.6e-5 of the result's norm.
 //  * kExact, the codes as bf16 (exact, two by one v_cvt_scalef32_pk_bf16_fp8)
-//    through four v_mfma_f32_16x16x32_bf16, whose sums keep fp32 (5e-8), at
-//    half the matrix rate.
-// Results in fp32 are kExact. Results in bf16, whose rounding (2^-9 on average
-// of its value) is a hundred times the native sums' error, are kNative where
-// the matrix cores bound the product and kExact where the weight stream does.
+//    through four v_mfma_f32_16x16x32_bf16, whose sums keep fp32: 1e-8 to 8e-8
+//    of the result's norm over a block, and a block's integers under 2^24 come
+//    out as they are. Results of both types are made so.
+//  * kNative, one v_mfma_f32_16x16x128_f8f6f4 at twice the rate, where the
+//    caller asks for fast sums (tiles only). Every e4m3 instruction aligns each
+//    eight neighbouring products to the largest of them and cuts what lies 13
+//    bits below (2^16 + 2^2 in one group of eight gives 2^16, in two groups
+//    2^16 + 2^2; v_mfma_f32_16x16x32_fp8_fp8 the same). Measured over a block:
+//    1.5e-5 of the norm on normal data, 4e-5 with a few strong channels, 5e-5 on
+//    uniform codes; a group that cancels (448^2 - 448^2 + 6 * 4) loses all.
+//    That is less than a rounding to bf16, so it goes with bf16 results alone.
 // bf16 operands (kBf16) take two v_mfma_f32_16x16x32_bf16 a block.
 // The rates that bound them on this card, with random operands from registers:
-// e4m3 3.65 PFLOP/s with the fma beside it, bf16 1.76.
+// kNative 3.65 PFLOP/s with the fma beside it, bf16 instructions 1.8 to 1.9.
 #include <type_traits>
 
 #include "fp8_internal.h"
@@ -907,25 +909,25 @@ int launch_stream(const ProductArgs &a, hipStream_t s) {
 
 int launch_fp8_dense(const ProductArgs &a, void *stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const fp8::DensePlan plan = fp8::dense_plan(a.rows, a.n, a.k_bytes, a.y_bf16);
+  const fp8::DensePlan plan = fp8::dense_plan(a.rows, a.n, a.k_bytes, a.fast);
   if (plan.stream) return launch_stream(a, s);
   switch (plan.tile) {
     case fp8::kTile32:
-      return a.y_bf16 ? launch_dense<Tile32, kNative>(a, plan, s) : launch_dense<Tile32, kExact>(a, plan, s);
+      return a.fast ? launch_dense<Tile32, kNative>(a, plan, s) : launch_dense<Tile32, kExact>(a, plan, s);
     case fp8::kTile64:
-      return a.y_bf16 ? launch_dense<Tile64, kNative>(a, plan, s) : launch_dense<Tile64, kExact>(a, plan, s);
+      return a.fast ? launch_dense<Tile64, kNative>(a, plan, s) : launch_dense<Tile64, kExact>(a, plan, s);
     case fp8::kTile128:
-      return a.y_bf16 ? launch_dense<Tile128, kNative>(a, plan, s) : launch_dense<Tile128, kExact>(a, plan, s);
+      return a.fast ? launch_dense<Tile128, kNative>(a, plan, s) : launch_dense<Tile128, kExact>(a, plan, s);
     case fp8::kTile256:
-      return a.y_bf16 ? launch_dense<Tile256, kNative>(a, plan, s) : launch_dense<Tile256, kExact>(a, plan, s);
+      return a.fast ? launch_dense<Tile256, kNative>(a, plan, s) : launch_dense<Tile256, kExact>(a, plan, s);
     default: return launch_dense<Tile256Wide, kNative>(a, plan, s);
   }
 }
 
 int launch_fp8_grouped(const ProductArgs &a, void *stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const int tile = fp8::grouped_tile(a.rows, a.n_experts, a.n, a.nb, !a.y_bf16);
-  return a.y_bf16 ? launch_grouped<kNative>(tile, a, s) : launch_grouped<kExact>(tile, a, s);
+  const int tile = fp8::grouped_tile(a.rows, a.n_experts, a.n, a.nb, !a.fast);
+  return a.fast ? launch_grouped<kNative>(tile, a, s) : launch_grouped<kExact>(tile, a, s);
 }
 
 int launch_bf16_grouped(const ProductArgs &a, void *stream) {

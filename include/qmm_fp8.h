@@ -23,13 +23,21 @@
  * The products below are
  *   y[r][i] = sum_b x_scale[b][r] * w_scale[i/128][b] *
  *             sum_{k in block b} x[r][k] * w[i][k],
- * with fp32 sums, y rounded once to its type (nearest even). With y in fp32 the
- * codes go through the matrix cores as bf16 (exact). With y in bf16 the e4m3
- * instruction may be used, which cuts products 13 bits below the largest of
- * each eight neighbours along k: about 2e-5 of the result's norm, a hundredth
- * of the rounding to bf16. Values
- * that are not finite go through as arithmetic has them: a NaN code or a NaN or
- * infinite scale makes the sums it enters NaN or infinite and touches no other.
+ * with fp32 sums, y rounded once to its type (nearest even). The product of the
+ * two scales is formed first, in fp32. The codes go through the matrix cores as
+ * bf16, which holds them exactly: every product is exact, and the sums lose what
+ * fp32 additions lose.
+ *
+ * QMM_FAST_SUMS, with y in bf16, lets a call take the e4m3 matrix instruction
+ * instead, at about twice the rate for many rows. It aligns each eight
+ * neighbouring products along k to the largest of them and cuts what lies 13
+ * bits below: a result is off by up to 7 * 2^-13 * sum |x w| before it is rounded
+ * (eight products that cancel can lose their sum), on normal data by 1.5e-5 and
+ * with a few strong channels by 4e-5 of the results' norm.
+ *
+ * Values that are not finite go through as arithmetic has them: a NaN code or a
+ * NaN or infinite scale makes the sums it enters NaN or infinite and touches no
+ * other.
  */
 #ifndef QMM_FP8_H
 #define QMM_FP8_H
@@ -43,6 +51,8 @@ extern "C" {
 /* ---- types of y, and of the rows given to the quantisers ---------------- */
 #define QMM_F32   0
 #define QMM_BF16  1
+#define QMM_FAST_SUMS 16   /* QMM_BF16 | QMM_FAST_SUMS: a y_type of qmm_fp8,
+                              qmm_fp8_workspace and qmm_fp8_grouped        */
 
 /* ---- limits (QMV_ERR_RANGE above) ---------------------------------------- */
 #define QMM_MAX_ROWS    (1 << 24)   /* rows of x or y of one call               */
@@ -83,14 +93,17 @@ size_t qmm_fp8_workspace(int m, int n, int k, int y_type);
  *   w, w_scale   e4m3 [n][k], 16-byte aligned, w_bytes == n*k;
  *                fp32 [ceil(n/128)][ceil(k/128)], 4-byte aligned
  *   x, x_scale   e4m3 [m][k], 16-byte aligned; fp32 [ceil(k/128)][m]
- *   y            [m][n] of y_type (QMM_F32 or QMM_BF16), 16-byte aligned
+ *   y            [m][n] of y_type (QMM_F32, QMM_BF16 or QMM_BF16 |
+ *                QMM_FAST_SUMS), 16-byte aligned
  *   ws           device memory of ws_bytes >= qmm_fp8_workspace(m, n, k, y_type),
  *                256-byte aligned (its contents do not matter); may be NULL
  *                when that size is 0, else QMV_ERR_WORKSPACE
  *   m >= 1, n >= 1, k >= 16 and k % 16 == 0
- * The order of the sums depends on (m, n, k, y_type) alone; for m <= QMM_SAME_ROWS
- * it depends on (n, k) alone, so a row has the same bits whatever m is (plain
- * decode and speculative verify run one numerical program).
+ * The order of the sums depends on m, n, k and QMM_FAST_SUMS alone; for m <=
+ * QMM_SAME_ROWS it depends on (n, k) alone, so a row has the same bits whatever m
+ * is (plain decode and speculative verify run one numerical program; fast sums
+ * have no effect there). From more rows on the order of a row's sums may change
+ * with m.
  */
 int qmm_fp8(const void *w, size_t w_bytes, const float *w_scale, const void *x, const float *x_scale,
             void *y, int y_type, int m, int n, int k, void *ws, size_t ws_bytes, void *stream);
