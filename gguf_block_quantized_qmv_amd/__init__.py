@@ -488,6 +488,7 @@ _E4M3 = (_torch().float8_e4m3fn, _torch().uint8)
 _BF16 = _bf16_types()
 _FLOATS = {_torch().float32: 0, _torch().bfloat16: 1}   # QMM_F32, QMM_BF16
 _FAST_SUMS = 16                                         # QMM_FAST_SUMS
+_MAX_ROWS = 1 << 24                                     # QMM_MAX_ROWS
 
 
 def _explain(t, name, types, shape, index):
@@ -507,7 +508,13 @@ def _take(t, name, types, shape, index):
     _explain(t, name, types, shape, index)
 
 
-def _first(x, name, types, dims):
+def _rows_in_range(rows, where):
+    # refused here as the C entry does: a C int would take rows modulo 2^32
+    if rows > _MAX_ROWS:
+        raise QmvError(-5, where)
+
+
+def _first(x, name, types, dims, where):
     """Device index and shape of the tensor that the others go by (its address is taken, and checked, later)."""
     try:
         index, shape = x.get_device(), x.shape
@@ -516,6 +523,7 @@ def _first(x, name, types, dims):
     if index < 0 or len(shape) != dims:
         _dev(x, name, tuple(types))
         raise ValueError(f"{name} has {x.dim()} dimensions, expected {dims}")
+    _rows_in_range(shape[0], where)
     return index, shape
 
 
@@ -539,7 +547,7 @@ def _run(fn, name, index, stream, *args):
 
 def _quant(fn, name, x, gated, xq, xs, stream):
     torch = _torch()
-    index, (m, k) = _first(x, "x", _FLOATS, 2)
+    index, (m, k) = _first(x, "x", _FLOATS, 2, name)
     if gated:
         if k % 2:
             raise ValueError(f"{name}: x must be [m, 2 k], got {(m, k)}")
@@ -577,7 +585,8 @@ def _type_code(dtype, fast_sums):
 
 def qmm_fp8_workspace(m: int, n: int, k: int, out_dtype=None, fast_sums: bool = False) -> int:
     """Bytes of ws a qmm_fp8 call of this shape needs (y fp32 unless out_dtype says bf16)."""
-    return lib.qmm_fp8_workspace(m, n, k, 0 if out_dtype is None else _type_code(out_dtype, fast_sums))
+    code = 0 if out_dtype is None else _type_code(out_dtype, fast_sums)
+    return 0 if max(m, n, k) > _MAX_ROWS else lib.qmm_fp8_workspace(m, n, k, code)   # out of range: 0, as in C
 
 
 def _y_type(y, out_dtype, fast_sums=False):
@@ -599,7 +608,7 @@ def qmm_fp8(w, w_scale, x, x_scale, n: int, k: int, y=None, out_dtype=None, ws=N
     which cuts partial sums (QMM_FAST_SUMS in qmm_fp8.h).
     """
     torch = _torch()
-    index, (m, _) = _first(x, "x", _E4M3, 2)
+    index, (m, _) = _first(x, "x", _E4M3, 2, "qmm_fp8")
     if y is None:
         with torch.cuda.stream(stream):   # memory of the stream that writes it
             y = torch.empty((m, n), dtype=out_dtype or torch.float32, device=x.device)
@@ -619,12 +628,13 @@ def qmm_fp8(w, w_scale, x, x_scale, n: int, k: int, y=None, out_dtype=None, ws=N
 
 def _grouped(fn, name, types, w, w_scale, x, x_scale, offsets, n, k, row_index, y, out_dtype, stream, fast_sums=False):
     torch = _torch()
-    index, (x_rows, _) = _first(x, "x", types, 2)
-    _, (e, _, _) = _first(w, "w", types, 3)
+    index, (x_rows, _) = _first(x, "x", types, 2, name)
+    _, (e, _, _) = _first(w, "w", types, 3, name)
     rows = x_rows
     found = None
     if row_index is not None:
         rows = row_index.numel()
+        _rows_in_range(rows, name)
         found = _take(row_index, "row_index", _I32, (rows,), index)
     if y is None:
         # rows that belong to no expert are not written: zeros there rather than what the memory held
