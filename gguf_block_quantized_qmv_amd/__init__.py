@@ -618,11 +618,12 @@ def qmm_fp8(w, w_scale, x, x_scale, n: int, k: int, y=None, out_dtype=None, ws=N
         if need:
             with torch.cuda.stream(stream):
                 ws = torch.empty(need, dtype=torch.uint8, device=x.device)
-    _run(lib.qmm_fp8, "qmm_fp8", index, stream,
-         _take(w, "w", _E4M3, (n, k), index), n * k, _take(w_scale, "w_scale", _F32, (_blocks(n), _blocks(k)), index),
-         _take(x, "x", _E4M3, (m, k), index), _take(x_scale, "x_scale", _F32, (_blocks(k), m), index),
-         _take(y, "y", _FLOATS, (m, n), index), y_type, m, n, k,
-         None if ws is None else _take(ws, "ws", _U8, ws.shape, index), 0 if ws is None else ws.numel())
+    args = (_take(w, "w", _E4M3, (n, k), index), n * k, _take(w_scale, "w_scale", _F32, (_blocks(n), _blocks(k)), index),
+            _take(x, "x", _E4M3, (m, k), index), _take(x_scale, "x_scale", _F32, (_blocks(k), m), index),
+            _take(y, "y", _FLOATS, (m, n), index), y_type, m, n, k,
+            None if ws is None else _take(ws, "ws", _U8, ws.shape, index), 0 if ws is None else ws.numel())
+    if m:   # no rows: y is empty, as from the grouped products
+        _run(lib.qmm_fp8, "qmm_fp8", index, stream, *args)
     return y
 
 

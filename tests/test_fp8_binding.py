@@ -66,3 +66,15 @@ def test_more_rows_than_a_c_int_are_refused(calls, refused):
     for shape in ((HUGE + 300, 5120, 17408), (300, HUGE + 5120, 17408), (300, 5120, HUGE + 17403)):
         assert q.qmm_fp8_workspace(*shape) == 0
     assert q.qmm_fp8_workspace(300, 5120, 17408) > 0
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_an_empty_batch_gives_an_empty_result(calls, dtype):
+    # as the grouped products and the quantisers: the C entry is for m >= 1
+    y = Fake((0, 64), dtype, address=0)
+    assert q.qmm_fp8(Fake((64, 128)), Fake((1, 1), torch.float32), Fake((0, 128), address=0),
+                     Fake((1, 0), torch.float32, address=0), 64, 128, y=y) is y
+    assert calls == []
+    with pytest.raises(ValueError, match="w has shape"), pytest.MonkeyPatch.context() as p:
+        p.setattr(q, "_dev", lambda *a: None)
+        q.qmm_fp8(Fake((65, 128)), Fake((1, 1), torch.float32), Fake((0, 128)), Fake((1, 0), torch.float32), 64, 128, y=y)

@@ -113,3 +113,12 @@ def test_a_bank_beyond_4_gib(q, dev, kind, fast, out):
     grouped(q, kind, fast, w[-1:].clone(), None if ws is None else ws[-1:].clone(), x, xs,
             torch.tensor([0, rows], dtype=torch.int32, device=dev), n, k, alone)
     assert same_bits(y, alone) and bool(torch.isfinite(alone).all()) and bool((alone != 0).any())
+
+
+@pytest.mark.parametrize("out", [F32, BF16])
+def test_an_empty_batch_runs_through_a_layer(q, dev, out):
+    w, ws = torch.zeros(256, 128, dtype=E4M3, device=dev), torch.ones(2, 1, device=dev)
+    down, ds = torch.zeros(64, 128, dtype=E4M3, device=dev), torch.ones(1, 1, device=dev)
+    y = q.qmm_fp8(w, ws, *q.qmm_fp8_quant(torch.empty(0, 128, dtype=out, device=dev)), 256, 128, out_dtype=out)
+    z = q.qmm_fp8(down, ds, *q.qmm_fp8_quant_silu_mul(y), 64, 128, out_dtype=out)
+    assert y.shape == (0, 256) and z.shape == (0, 64) and z.dtype == out
