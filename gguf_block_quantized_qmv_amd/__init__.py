@@ -585,7 +585,9 @@ def _type_code(dtype, fast_sums):
 
 def qmm_fp8_workspace(m: int, n: int, k: int, out_dtype=None, fast_sums: bool = False) -> int:
     """Bytes of ws a qmm_fp8 call of this shape needs (y fp32 unless out_dtype says bf16)."""
-    code = 0 if out_dtype is None else _type_code(out_dtype, fast_sums)
+    if out_dtype is not None and out_dtype not in _FLOATS:
+        raise TypeError(f"out_dtype is {out_dtype}, expected float32 or bfloat16")
+    code = _type_code(out_dtype or _F32[0], fast_sums)
     return 0 if max(m, n, k) > _MAX_ROWS else lib.qmm_fp8_workspace(m, n, k, code)   # out of range: 0, as in C
 
 

@@ -78,3 +78,10 @@ def test_an_empty_batch_gives_an_empty_result(calls, dtype):
     with pytest.raises(ValueError, match="w has shape"), pytest.MonkeyPatch.context() as p:
         p.setattr(q, "_dev", lambda *a: None)
         q.qmm_fp8(Fake((65, 128)), Fake((1, 1), torch.float32), Fake((0, 128)), Fake((1, 0), torch.float32), 64, 128, y=y)
+
+
+def test_workspace_of_a_type_that_is_no_result(calls):
+    for dtype in (torch.float16, torch.uint8, "bf16"):
+        with pytest.raises(TypeError, match="float32 or bfloat16"):
+            q.qmm_fp8_workspace(300, 5120, 17408, dtype)
+    assert q.qmm_fp8_workspace(300, 5120, 17408, torch.bfloat16) == q.qmm_fp8_workspace(300, 5120, 17408)
