@@ -527,11 +527,19 @@ def _first(x, name, types, dims, where):
     return index, shape
 
 
+def _current_stream(index):
+    return _torch().cuda.current_stream(index).cuda_stream
+
+
+# the same without the stream's object, where torch has it: a decode step makes many calls
+_current_stream = getattr(_torch()._C, "_cuda_getCurrentRawStream", _current_stream)
+
+
 def _run(fn, name, index, stream, *args):
     """Calls the C entry point on the tensors' own device, on its current stream unless one is given."""
     torch = _torch()
     if stream is None:
-        raw = torch._C._cuda_getCurrentRawStream(index)   # torch.cuda.current_stream(index) without its object
+        raw = _current_stream(index)
     elif stream.device_index != index:
         raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
     else:

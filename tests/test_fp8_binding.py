@@ -1,5 +1,9 @@
 """The e4m3 binding without a GPU, on stand-in tensors and a stand-in library: what reaches the C entry points."""
 
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -36,6 +40,7 @@ def calls(monkeypatch):
     return seen
 
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 HUGE = (1 << 32) + 5   # a C int of this value is 5
 
 
@@ -85,3 +90,22 @@ def test_workspace_of_a_type_that_is_no_result(calls):
         with pytest.raises(TypeError, match="float32 or bfloat16"):
             q.qmm_fp8_workspace(300, 5120, 17408, dtype)
     assert q.qmm_fp8_workspace(300, 5120, 17408, torch.bfloat16) == q.qmm_fp8_workspace(300, 5120, 17408)
+
+
+def test_the_binding_needs_no_private_name_of_torch():
+    # the current stream's handle by torch's public call when its short one is gone
+    code = """
+import torch
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+    del torch._C._cuda_getCurrentRawStream
+import gguf_block_quantized_qmv_amd as q
+class Stream:
+    cuda_stream = 77
+torch.cuda.current_stream = lambda index: Stream() if index == 3 else None
+torch.cuda.current_device = lambda: 3
+seen = []
+q._run(lambda *a: seen.append(a) or 0, "call", 3, None, 1, 2)
+assert seen == [(1, 2, 77)], seen
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300, cwd=ROOT)
+    assert r.returncode == 0, r.stderr
