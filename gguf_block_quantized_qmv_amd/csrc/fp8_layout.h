@@ -44,7 +44,7 @@ struct DensePlan {
 // against 26.9 by tiles of 32 rows); with more of them while the weights are
 // small (77 x 1000 x 2064: 8 us against 14; 32 x 17408 x 5120: 56 against 33).
 constexpr int64_t kStreamBytes = (int64_t)32 << 20;
-constexpr int kStreamRows = 2048;   // 512 x 1024 x 1024: 13.8 us against 14.5
+constexpr int kStreamRows = 2048;   // 512 x 1024 x 1024: 15.4 us against 16.7
 
 inline DensePlan split_plan(int tile, int m, int n, int nb) {
   DensePlan p{false, tile, 0, 0, 1};
@@ -128,8 +128,11 @@ inline StreamPlan stream_plan(int m, int n, int nb) {
 // least time by this model, in ns: a step of one block of k takes 700 (32 x 64,
 // four workgroups a CU), 900 (64 x 128, two), 750 (128 x 128) and 1800 (256 x
 // 256), for codes widened to bf16 (`exact`: e4m3 without fast sums) 900, 1200
-// and 2200 (256 x 128); a tile starts and ends in 6000. (8 rows, 8 of 128 experts of 1536 x 2048: 8.5 us by 32 x 64,
-// 11.4 by 64 x 128, 10.1 by 128 x 128; 4096 rows: 102, 84, 88.)
+// and 2200 (256 x 128); a tile starts and ends in 6000. Measured, in us: with
+// fast sums 8 rows, 8 of 128 experts of 1536 x 2048, 8.5 by 32 x 64, 11.4 by 64 x
+// 128, 10.1 by 128 x 128, and 4096 rows 102, 84, 88; widened 8 rows 10 by 32 x
+// 64, 17 by 64 x 128, 20 by 256 x 128, 4096 rows 106, 104, 131, and 65536 rows of
+// 2048 x 768 480, 321, 282.
 inline int grouped_tile(int rows, int n_experts, int n, int nb, bool exact) {
   const int busy = rows < n_experts ? rows : n_experts;
   int best = kTile32;

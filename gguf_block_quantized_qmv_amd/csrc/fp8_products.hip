@@ -22,7 +22,8 @@
 //    2^16 + 2^2; v_mfma_f32_16x16x32_fp8_fp8 the same). Measured over a block:
 //    1.5e-5 of the norm on normal data, 4e-5 with a few strong channels, 5e-5 on
 //    uniform codes; a group that cancels (448^2 - 448^2 + 6 * 4) loses all.
-//    That is less than a rounding to bf16, so it goes with bf16 results alone.
+//    But for such groups that is less than a rounding to bf16, so it goes with
+//    bf16 results alone.
 // bf16 operands (kBf16) take two v_mfma_f32_16x16x32_bf16 a block.
 // The rates that bound them on this card, with random operands from registers:
 // kNative 3.65 PFLOP/s with the fma beside it, bf16 instructions 1.8 to 1.9.
@@ -129,9 +130,9 @@ __device__ __forceinline__ void expert_rows(const int32_t *__restrict__ offsets,
 // work, no memory traffic). The order of the sums goes by (n, k) alone and the columns
 // of an MFMA do not mix, so a row of x has the same bits in any company.
 //
-// Bound by the weight stream: 1 x 17408 x 5120 takes 17.4 us with the weights
+// Bound by the weight stream: 1 x 17408 x 5120 takes 17.5 us with the weights
 // partly in the last-level cache (5.1 TB/s; a plain read of as many bytes 17.6
-// us from HBM) and 22.9 us from HBM. What counted: two fragments of w for one
+// us from HBM) and 21.4 to 23 us from HBM. What counted: two fragments of w for one
 // of x (MW = 1 reads as many bytes of x as of w through the L2: 26.5 us), and
 // plain loads (a fragment takes a 128-byte line in two halves: with
 // non-temporal loads each half fetched the line, 23.7 us). Matrices of less
@@ -267,21 +268,24 @@ __global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(4))) vo
 //    1, 3 and 4 of r.
 //
 // What bounds it, and why these shapes:
-//  * Long products: the matrix cores and their power. 4096 x 17408 x 5120 in
-//    bf16 takes 322 to 338 us, 2.2 PFLOP/s; the same call on zeros takes a fifth
-//    less. Of the shapes only 256 x 256 (waves of 128 x 64) asks LDS for no
-//    more than it gives beside the matrix instructions; a step of it takes 1.8
-//    us, two of 256 x 128 (waves of 64 x 64) take 2.3. Its sums fill the
-//    registers at two waves a SIMD, and two stages fill LDS.
-//  * fp32 results: 700 us, 1.04 PFLOP/s; two conversions for each bf16 matrix
-//    instruction share the issue slots with the fma.
-//  * Few steps a tile (k of 768): the stores. 65536 rows over 128 experts, n
-//    2048: 187 to 196 us, of which 50 are the 268 MB of y at the card's write rate;
-//    the loads of a following tile beyond its first blocks queue behind them.
-//    Smaller tiles, two workgroups a CU, overlap them and lose more to LDS
-//    (128 x 128: 224 us).
+//  * Long products: the conversions. 4096 x 17408 x 5120 takes 600 to 633 us,
+//    1.15 to 1.2 PFLOP/s, the matrix cores 58 % busy: two conversions for each of
+//    their instructions share the issue slots with the fma. A widened operand
+//    takes twice the registers, so 256 x 128 is the largest tile.
+//  * With fast sums, the matrix cores and their power: 309 to 336 us, 2.2 to 2.4
+//    PFLOP/s, 59 % busy; on zeros a fifth less. Of the shapes only 256 x 256
+//    (waves of 128 x 64) asks LDS for no more than it gives beside the matrix
+//    instructions; a step of it takes 1.8 us, two of 256 x 128 (waves of
+//    64 x 64) take 2.3. Its sums fill the registers at two waves a SIMD, and two
+//    stages fill LDS.
+//  * Few steps a tile (k of 768): the stores beside them. 65536 rows over 128
+//    experts, n 2048, bf16 results: 281 to 289 us, with fast sums 182 to 190, of
+//    which 50 are the 268 MB of y at the card's write rate; the loads of a
+//    following tile beyond its first blocks queue behind them. Smaller tiles, two
+//    workgroups a CU, overlap them and lose more to LDS (64 x 128: 321 us; fast
+//    sums by 128 x 128: 224 us).
 //  * Few rows: the weight stream. 512 tokens to 8 of 128 experts of 1536 x
-//    2048: 86 us for 417 MB, by 64 x 128 tiles, two workgroups a CU.
+//    2048: 89 us for 417 MB, by 64 x 128 tiles, two workgroups a CU.
 // Without effect or slower: weight scales through LDS, a rotated first block
 // per workgroup, other places for the loads in a step, non-temporal loads or
 // stores, a wait that leaves the stores of the tile before under way.
@@ -554,7 +558,8 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
   for (;;) {
     // A wave whose rows all lie behind the tile's last one brings its share of
     // the stages and multiplies nothing: the matrix cores of its SIMD are the
-    // other wave's (65536 rows over 128 experts, n 2048, k 768: 193 us, 189).
+    // other wave's (65536 rows over 128 experts, n 2048, k 768, fast
+    // sums: 193 us, 189).
     if (GROUPED && S::WM > 1 && t.m0 + wm * S::TM * 16 >= t.end) {
       for (int b = t.blk0; b < t.blk1; ++b) {
         if (b + kAhead < t.blk1) {
@@ -802,7 +807,7 @@ __global__ __launch_bounds__(S::kThreads) void product_tile_kernel(const Product
 // y of the tiles that were cut along k: the parts in the order of k, a lane's
 // four or eight neighbouring columns a thread. Bound by the parts' bytes, read
 // once and past the caches that the next call's operands use (512 x 5120 x
-// 17408: the whole call 58.7 us with plain loads, 57.1 so).
+// 17408, fast sums: the whole call 58.7 us with plain loads, 57.1 so).
 template <class S>
 __global__ __launch_bounds__(256) void product_sum_kernel(const ProductArgs p, const int t_main, const int r_tiles,
                                                           const int splits) {
