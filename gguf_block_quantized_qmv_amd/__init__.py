@@ -610,7 +610,8 @@ def _y_type(y, out_dtype, fast_sums=False):
 def qmm_fp8(w, w_scale, x, x_scale, n: int, k: int, y=None, out_dtype=None, ws=None, stream=None,
             fast_sums: bool = False):
     """y[m, n] = x @ w^T for e4m3 w [n, k] and x [m, k] with scales w_scale [ceil(n/128), ceil(k/128)] and
-    x_scale [ceil(k/128), m] (as qmm_fp8_quant gives them); y is fp32 unless y or out_dtype says bf16.
+    x_scale [ceil(k/128), m] (as qmm_fp8_quant gives them); y is fp32 unless y or out_dtype says bf16. Without rows
+    (m = 0) nothing is launched.
 
     ws: None allocates the workspace the shape needs (if any), or a uint8 device
     tensor of at least qmm_fp8_workspace(m, n, k, y.dtype, fast_sums) bytes to reuse.

@@ -122,3 +122,33 @@ def test_an_empty_batch_runs_through_a_layer(q, dev, out):
     y = q.qmm_fp8(w, ws, *q.qmm_fp8_quant(torch.empty(0, 128, dtype=out, device=dev)), 256, 128, out_dtype=out)
     z = q.qmm_fp8(down, ds, *q.qmm_fp8_quant_silu_mul(y), 64, 128, out_dtype=out)
     assert y.shape == (0, 256) and z.shape == (0, 64) and z.dtype == out
+
+
+@pytest.mark.parametrize("kind,fast,out", KINDS)
+def test_a_captured_call_follows_the_routing_that_it_finds(q, dev, kind, fast, out):
+    # offsets and row indexes are read on the device: a replay takes those that are there by then
+    n, k, rows, e = 520, 400, 700, 9
+    g = torch.Generator(device=dev).manual_seed(5)
+    w, ws, x, xs = operands(g, dev, kind, e, n, k, 200)
+    index, off = torch.zeros(rows, dtype=torch.int32, device=dev), torch.zeros(e + 1, dtype=torch.int32, device=dev)
+    y = torch.empty(rows, n, dtype=out, device=dev)
+    off[1:] = rows
+    grouped(q, kind, fast, w, ws, x, xs, off, n, k, y, index)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        grouped(q, kind, fast, w, ws, x, xs, off, n, k, y, index)
+    routings = ([0] * 10, [0, 700] + [700] * 8, [3, 3, 4, 260, 260, 517, 580, 581, 690, 695], list(range(0, 700, 70)),
+                [0] * 9 + [700])
+    for bounds in routings:
+        off.copy_(torch.tensor(bounds, dtype=torch.int32))
+        index.copy_(torch.randint(-3, 205, (rows,), generator=g, device=dev, dtype=torch.int32))
+        want = torch.full_like(y, -7.0)
+        grouped(q, kind, fast, w, ws, x, xs, off, n, k, want, index)
+        y.fill_(-7.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same_bits(y, want), bounds
+        assert bool((want[:bounds[0]] == -7.0).all() and (want[bounds[-1]:] == -7.0).all())
