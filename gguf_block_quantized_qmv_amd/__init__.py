@@ -2,7 +2,8 @@
 
 Argument marshalling only: every function below checks tensor dtypes/devices,
 takes device pointers and torch's current stream, and calls the C entry point of
-the same name declared in include/qmv.h or include/qmm_fp8.h. All computation happens in the HIP
+the same name declared in include/qmv.h, include/qmm_fp8.h, include/qmm_rows.h or
+include/qmv_verify.h. All computation happens in the HIP
 kernels of the library; there is no fallback path. Importing this package
 without a built library raises ImportError.
 """
@@ -25,6 +26,9 @@ __all__ = [
     "iq4_xs_bytes", "EXPORTS",
     "qmm_fp8_quant", "qmm_fp8_quant_silu_mul", "qmm_fp8", "qmm_fp8_workspace", "qmm_fp8_grouped", "qmm_bf16_grouped",
     "FP8_EXPORTS",
+    "qmm_rows_sort", "qmm_rows_sort_workspace", "qmm_rows_spread", "qmm_rows_combine", "qmm_rows_combine_grad",
+    "qmm_lora", "qmm_lora_workspace", "qmv_verify_drafts", "qmv_verify_drafts_workspace",
+    "ROWS_EXPORTS", "VERIFY_EXPORTS",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqmv.so")
@@ -78,6 +82,24 @@ FP8_EXPORTS = {
                                   _vp]),
 }
 
+# name -> (restype, argtypes); mirrors include/qmm_rows.h
+ROWS_EXPORTS = {
+    "qmm_rows_sort_workspace": (_c_size, [_c_int, _c_int, _c_int]),
+    "qmm_rows_sort": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _vp, _c_size, _vp]),
+    "qmm_rows_spread": (_c_int, [_vp, _c_int, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp]),
+    "qmm_rows_combine": (_c_int, [_vp, _c_int, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp]),
+    "qmm_rows_combine_grad": (_c_int, [_vp, _vp, _c_int, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _vp]),
+    "qmm_lora_workspace": (_c_size, [_c_int, _c_int, _c_int, _c_int, _c_int]),
+    "qmm_lora": (_c_int, [_vp, _c_size, _vp, _c_size, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int,
+                          _c_int, _c_int, _c_int, _vp, _c_size, _vp]),
+}
+
+# name -> (restype, argtypes); mirrors include/qmv_verify.h
+VERIFY_EXPORTS = {
+    "qmv_verify_drafts_workspace": (_c_size, [_c_int, _c_int]),
+    "qmv_verify_drafts": (_c_int, [_vp, _vp, _c_int, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _vp, _c_size, _vp]),
+}
+
 
 def _load():
     # torch's HIP build ships its own libamdhip64 (same soname as the system one).
@@ -91,7 +113,7 @@ def _load():
             f"{LIB_PATH} is not built; run `python gguf_block_quantized_qmv_amd/build.py` "
             "(or __graft_entry__.build()) first")
     handle = ctypes.CDLL(LIB_PATH)
-    for name, (res, args) in (*EXPORTS.items(), *FP8_EXPORTS.items()):
+    for name, (res, args) in (*EXPORTS.items(), *FP8_EXPORTS.items(), *ROWS_EXPORTS.items(), *VERIFY_EXPORTS.items()):
         fn = getattr(handle, name)
         fn.restype = res
         fn.argtypes = args
@@ -681,3 +703,216 @@ def qmm_bf16_grouped(w, x, offsets, n: int, k: int, row_index=None, y=None, out_
     """As qmm_fp8_grouped on bf16 w [experts, n, k] and x [x_rows, k]."""
     return _grouped(lib.qmm_bf16_grouped, "qmm_bf16_grouped", _BF16, w, None, x, None, offsets, n, k, row_index, y,
                     out_dtype, stream)
+
+
+# ---------------------------------------------------------------- rows by expert or adapter, drafts
+
+def _in_c(where, *sizes):
+    # as _rows_in_range, for every other size: what a C int cannot hold is refused here
+    if max(sizes) > _MAX_ROWS:
+        raise QmvError(-5, where)
+
+
+def _new(shape, dtype, device, stream, zeros=False):
+    """Memory of the stream that writes it."""
+    torch = _torch()
+    with torch.cuda.stream(stream):
+        return (torch.zeros if zeros else torch.empty)(shape, dtype=dtype, device=device)
+
+
+def _work_memory(ws, need, device, index, stream):
+    """Address and size of the workspace, made where a call needs one and has none."""
+    if ws is None:
+        if not need:
+            return None, 0
+        ws = _new(need, _U8[0], device, stream)
+    return _take(ws, "ws", _U8, (ws.numel(),), index), ws.numel()
+
+
+def _or_none(t, name, types, shape, index):
+    return None if t is None else _take(t, name, types, shape, index)
+
+
+def qmm_rows_sort_workspace(tokens: int, top_k: int, n_experts: int) -> int:
+    """Bytes of ws a qmm_rows_sort call of this shape needs."""
+    return 0 if max(tokens, top_k, n_experts) > _MAX_ROWS else lib.qmm_rows_sort_workspace(tokens, top_k, n_experts)
+
+
+def qmm_rows_sort(ids, n_experts: int, offsets=None, row_index=None, places=None, ws=None, stream=None):
+    """Choices ids [tokens, top_k] (int32) sorted by expert; returns (offsets [n_experts + 1], row_index
+    [tokens * top_k], places [tokens, top_k]), all int32.
+
+    Rows offsets[e] .. offsets[e+1] - 1 are expert e's, row_index[r] is the token of row r (-1 from
+    offsets[n_experts] on) and places[t, j] the row of a choice (-1 where ids[t, j] lies outside [0, n_experts)).
+    ws: None allocates what the shape needs, or a uint8 device tensor of at least
+    qmm_rows_sort_workspace(tokens, top_k, n_experts) bytes to reuse.
+    """
+    name = "qmm_rows_sort"
+    index, (tokens, top_k) = _first(ids, "ids", _I32, 2, name)
+    _in_c(name, top_k, n_experts)
+    if n_experts < 1:
+        raise QmvError(-5, name)
+    if offsets is None:
+        offsets = _new((n_experts + 1,), _I32[0], ids.device, stream)
+    if row_index is None:
+        row_index = _new((tokens * top_k,), _I32[0], ids.device, stream)
+    if places is None:
+        places = _new((tokens, top_k), _I32[0], ids.device, stream)
+    args = (_take(ids, "ids", _I32, (tokens, top_k), index), _take(offsets, "offsets", _I32, (n_experts + 1,), index),
+            _take(row_index, "row_index", _I32, (tokens * top_k,), index),
+            _take(places, "places", _I32, (tokens, top_k), index))
+    wp, wn = _work_memory(ws, lib.qmm_rows_sort_workspace(tokens, top_k, n_experts), ids.device, index, stream)
+    _run(lib.qmm_rows_sort, name, index, stream, *args, tokens, top_k, n_experts, wp, wn)
+    return offsets, row_index, places
+
+
+def qmm_rows_spread(x, places, rows=None, out=None, stream=None):
+    """out [rows, h] with out[places[t, j]] = x[t] for x [tokens, h] (fp32 or bf16), places int32 [tokens, top_k].
+
+    rows: as many as places has unless out or rows says otherwise. Rows that no place names are left as they were
+    (zeros when out is None). The gradient by x is qmm_rows_combine(gradient of out, places).
+    """
+    name = "qmm_rows_spread"
+    index, (tokens, h) = _first(x, "x", _FLOATS, 2, name)
+    _, (_, top_k) = _first(places, "places", _I32, 2, name)
+    if out is not None:
+        _, (have, _) = _first(out, "out", (x.dtype,), 2, name)
+        if rows is not None and rows != have:
+            raise ValueError(f"out has {have} rows, expected {rows}")
+        rows = have
+    elif rows is None:
+        rows = tokens * top_k
+    _in_c(name, top_k, h, rows)
+    if out is None:
+        out = _new((rows, h), x.dtype, x.device, stream, zeros=True)
+    _run(lib.qmm_rows_spread, name, index, stream, _take(x, "x", _FLOATS, (tokens, h), index), _FLOATS[x.dtype],
+         _take(places, "places", _I32, (tokens, top_k), index), _take(out, "out", (x.dtype,), (rows, h), index), tokens,
+         top_k, h, rows)
+    return out
+
+
+def qmm_rows_combine(z, places, weights=None, y=None, out_dtype=None, stream=None):
+    """y [tokens, h] with y[t] = sum over j of weights[t, j] * z[places[t, j]], summed in fp32 in the order of j.
+
+    z [rows, h] fp32 or bf16, places int32 [tokens, top_k] (outside z: adds nothing), weights fp32 [tokens, top_k] or
+    None (ones); y is fp32 unless y or out_dtype says bf16.
+    """
+    name = "qmm_rows_combine"
+    index, (rows, h) = _first(z, "z", _FLOATS, 2, name)
+    _, (tokens, top_k) = _first(places, "places", _I32, 2, name)
+    _in_c(name, top_k, h)
+    if y is None:
+        y = _new((tokens, h), out_dtype or _F32[0], z.device, stream)
+    y_type = _y_type(y, out_dtype)
+    _run(lib.qmm_rows_combine, name, index, stream, _take(z, "z", _FLOATS, (rows, h), index), _FLOATS[z.dtype],
+         _take(places, "places", _I32, (tokens, top_k), index), _or_none(weights, "weights", _F32, (tokens, top_k), index),
+         _take(y, "y", _FLOATS, (tokens, h), index), y_type, tokens, top_k, h, rows)
+    return y
+
+
+def qmm_rows_combine_grad(dy, z, places, weights=None, rows=None, dz=None, dw=None, stream=None):
+    """Gradient of qmm_rows_combine from dy [tokens, h]: returns (dz [rows, h], dw [tokens, top_k] in fp32).
+
+    dz[places[t, j]] = weights[t, j] * dy[t], dw[t, j] = <dy[t], z[places[t, j]]> (0 without a place); dy, z and dz of one
+    type. z None: no dw (None comes back), dz has `rows` rows, as many as places unless it says otherwise. Rows of dz that
+    no place names are left as they were (zeros when dz is None).
+    """
+    name = "qmm_rows_combine_grad"
+    index, (tokens, h) = _first(dy, "dy", _FLOATS, 2, name)
+    _, (_, top_k) = _first(places, "places", _I32, 2, name)
+    same = (dy.dtype,)
+    for t, what in ((dz, "dz"), (z, "z")):
+        if t is not None:
+            _, (have, _) = _first(t, what, same, 2, name)
+            if rows is not None and rows != have:
+                raise ValueError(f"{what} has {have} rows, expected {rows}")
+            rows = have
+    if rows is None:
+        rows = tokens * top_k
+    if z is None and dw is not None:
+        raise ValueError("dw needs z")
+    _in_c(name, top_k, h, rows)
+    if dz is None:
+        dz = _new((rows, h), dy.dtype, dy.device, stream, zeros=True)
+    if dw is None and z is not None:
+        dw = _new((tokens, top_k), _F32[0], dy.device, stream)
+    _run(lib.qmm_rows_combine_grad, name, index, stream, _take(dy, "dy", _FLOATS, (tokens, h), index),
+         _or_none(z, "z", same, (rows, h), index), _FLOATS[dy.dtype], _take(places, "places", _I32, (tokens, top_k), index),
+         _or_none(weights, "weights", _F32, (tokens, top_k), index), _take(dz, "dz", same, (rows, h), index),
+         _or_none(dw, "dw", _F32, (tokens, top_k), index), tokens, top_k, h, rows)
+    return dz, dw
+
+
+def qmm_lora_workspace(rows: int, n: int, k: int, rank: int, n_adapters: int) -> int:
+    """Bytes of ws a qmm_lora call of this shape needs."""
+    sizes = (rows, n, k, rank, n_adapters)
+    return 0 if max(sizes) > _MAX_ROWS else lib.qmm_lora_workspace(*sizes)
+
+
+def qmm_lora(x, a, b, offsets, y, row_index=None, scale=None, ranks=None, base=None, ws=None, stream=None):
+    """y[r] = base[r] + scale[e] * b[e] @ (a[e] @ x[r]) for the rows r of each adapter e's run; returns y.
+
+    x [x_rows, k] bf16, a [n_adapters, rank, k] and b [n_adapters, n, rank] bf16, y and base [x_rows, n] fp32 or bf16
+    (base None: y itself, added to in place), scale fp32 [n_adapters] or None (ones), ranks int32 [n_adapters] or None
+    (rank). offsets and row_index as qmm_rows_sort(adapter of each row [x_rows, 1], n_adapters) gives them; row_index
+    None: rows stand in order. Rows without an adapter are left as they were in y.
+    ws: None allocates what the shape needs, or a uint8 device tensor of at least
+    qmm_lora_workspace(rows, n, k, rank, n_adapters) bytes to reuse.
+    """
+    name = "qmm_lora"
+    index, (x_rows, k) = _first(x, "x", _BF16, 2, name)
+    _, (e, rank, _) = _first(a, "a", _BF16, 3, name)
+    _, (_, n, _) = _first(b, "b", _BF16, 3, name)
+    rows, found = x_rows, None
+    if row_index is not None:
+        rows = row_index.numel()
+        _rows_in_range(rows, name)
+        found = _take(row_index, "row_index", _I32, (rows,), index)
+    _in_c(name, rank, k, n)
+    _first(y, "y", _FLOATS, 2, name)
+    y_type = _y_type(y, None)
+    yp = _take(y, "y", _FLOATS, (x_rows, n), index)
+    args = (_take(a, "a", _BF16, (e, rank, k), index), 2 * e * rank * k, _take(b, "b", _BF16, (e, n, rank), index),
+            2 * e * n * rank, _or_none(scale, "scale", _F32, (e,), index), _or_none(ranks, "ranks", _I32, (e,), index),
+            _take(x, "x", _BF16, (x_rows, k), index), _take(offsets, "offsets", _I32, (e + 1,), index), found,
+            yp if base is None else _take(base, "base", (y.dtype,), (x_rows, n), index), yp)
+    wp, wn = _work_memory(ws, lib.qmm_lora_workspace(rows, n, k, rank, e), x.device, index, stream)
+    if rows:   # an empty row_index has no address, which would stand for rows in order
+        _run(lib.qmm_lora, name, index, stream, *args, y_type, rows, x_rows, n, k, rank, e, wp, wn)
+    return y
+
+
+def qmv_verify_drafts_workspace(requests: int, vocab: int) -> int:
+    """Bytes of ws a qmv_verify_drafts call of this shape needs."""
+    return 0 if max(requests, vocab) > _MAX_ROWS else lib.qmv_verify_drafts_workspace(requests, vocab)
+
+
+def qmv_verify_drafts(p, drafts, u, q=None, lengths=None, accepted=None, tokens=None, ws=None, stream=None):
+    """Which drafted tokens stand, and the token that follows them: returns (accepted [requests], tokens
+    [requests, drafts + 1]), int32; a row of tokens holds the drafts that stand, the token that follows and -1s.
+
+    p [requests, drafts + 1, vocab]: the target's probabilities (fp32 or bf16); drafts int32 [requests, drafts]; u fp32
+    [requests, drafts + 1], uniform in [0, 1): u[r, i] decides on draft i, the last one picks. q [requests, drafts,
+    vocab], of p's type: the probabilities that the drafts were drawn from; None: each draft had all of them. lengths
+    int32 [requests]: the drafts that a request has (None: all).
+    ws: None allocates what the shape needs, or a uint8 device tensor of at least
+    qmv_verify_drafts_workspace(requests, vocab) bytes to reuse.
+    """
+    name = "qmv_verify_drafts"
+    index, (requests, steps, vocab) = _first(p, "p", _FLOATS, 3, name)
+    _in_c(name, steps, vocab)
+    if steps < 1:
+        raise ValueError(f"{name}: p must be [requests, drafts + 1, vocab], got {tuple(p.shape)}")
+    n = steps - 1
+    if accepted is None:
+        accepted = _new((requests,), _I32[0], p.device, stream)
+    if tokens is None:
+        tokens = _new((requests, steps), _I32[0], p.device, stream)
+    args = (_take(p, "p", _FLOATS, (requests, steps, vocab), index),
+            _or_none(q, "q", (p.dtype,), (requests, n, vocab), index), _FLOATS[p.dtype],
+            _take(drafts, "drafts", _I32, (requests, n), index), _or_none(lengths, "lengths", _I32, (requests,), index),
+            _take(u, "u", _F32, (requests, steps), index), _take(accepted, "accepted", _I32, (requests,), index),
+            _take(tokens, "tokens", _I32, (requests, steps), index))
+    wp, wn = _work_memory(ws, lib.qmv_verify_drafts_workspace(requests, vocab), p.device, index, stream)
+    _run(lib.qmv_verify_drafts, name, index, stream, *args, requests, n, vocab, wp, wn)
+    return accepted, tokens

@@ -22,8 +22,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqmv.so")
 
 HIP_SOURCES = ["q4k_gemv.hip", "q8_0.hip", "q4k_dequant.hip", "q4k_moe.hip", "q4k_prefill.hip", "iq4xs_gemv.hip", "iq4xs_moe.hip", "q6k_gemv.hip", "q4k_moe_grouped.hip", "calib_read.hip",
-               "fp8_quant.hip", "fp8_products.hip"]
-HOST_SOURCES = ["qmv_api.cpp", "fp8_api.cpp"]
+               "fp8_quant.hip", "fp8_products.hip", "rows_sort.hip", "rows_move.hip", "lora.hip", "verify.hip"]
+HOST_SOURCES = ["qmv_api.cpp", "fp8_api.cpp", "rows_api.cpp"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 HIP_FLAGS = [
