@@ -49,7 +49,8 @@ int check_move(int tokens, int top_k, int h, int rows) {
 int check_lora(int rows, int n, int k, int rank, int n_adapters) {
   if (rows < 0 || rows > QMM_MAX_ROWS || n_adapters < 1 || n_adapters > QMM_MAX_EXPERTS) return QMV_ERR_RANGE;
   if (n < 1 || k < 8 || k % 8 || rank < 8 || rank % 8) return QMV_ERR_SHAPE;
-  return n > QMM_MAX_N || k > QMM_MAX_K || rank > QMM_MAX_RANK ? QMV_ERR_RANGE : QMV_OK;
+  if (n > QMM_MAX_N || k > QMM_MAX_K || rank > QMM_MAX_RANK) return QMV_ERR_RANGE;
+  return qmv::rows::lora_in_grid(rows, n, n_adapters) ? QMV_OK : QMV_ERR_RANGE;
 }
 
 bool verify_ok(int requests, int vocab) {
@@ -189,7 +190,7 @@ int qmm_lora(const uint16_t *a, size_t a_bytes, const uint16_t *b, size_t b_byte
       !aligned(scale, 4) || !aligned(ranks, 4) || !aligned(offsets, 4) || !aligned(row_index, 4) || !aligned(ws, 256))
     return QMV_ERR_ALIGN;
   const size_t need = qmv::rows::lora_workspace(rows, n, k, rank, n_adapters);
-  if (!ws || ws_bytes < need) return QMV_ERR_WORKSPACE;
+  if (need && (!ws || ws_bytes < need)) return QMV_ERR_WORKSPACE;
   const size_t yb = (size_t)x_rows * n * type_bytes(y_type), eb = (size_t)n_adapters * 4;
   const Span all[] = {{y, yb},      {ws, need},   {a, ab},
                       {b, bb},      {scale, eb},  {ranks, eb},

@@ -44,33 +44,53 @@ inline size_t sort_workspace(int choices, int n_experts) {
 
 constexpr int kKBlock = 64;   // values of k a wave takes at a time
 
-// Rows of one tile (one adapter's), the parts of k of the first product and the
-// columns of y of one workgroup of the second. Up to QMM_SAME_ROWS rows all of
-// it goes by (n, k, rank) alone.
+// Rows of one tile (one adapter's), the parts of k of the first product, the
+// columns of y of one workgroup of the second, and whether y goes past the caches.
+// The sums of a row go by the parts alone, and up to QMM_SAME_ROWS rows these go by
+// k alone.
 struct LoraPlan {
   int tile, splits, columns;
+  bool far;
 };
 
 inline int lora_tiles(int rows, int n_adapters, int tile) {
   return rows / tile + (rows < n_adapters ? rows : n_adapters);
 }
 
-inline LoraPlan lora_plan(int rows, int n, int k, int rank, int n_adapters) {
-  (void)n;
-  const int blocks = ceil_div(k, kKBlock);
-  int most = blocks / 4 < 1 ? 1 : blocks / 4 > 16 ? 16 : blocks / 4;   // a block for each of four waves
-  if (rows <= QMM_SAME_ROWS) return LoraPlan{16, most, 256};
-  const bool many = rows / n_adapters >= 64;
-  const int tile = !many ? 16 : rank <= 64 ? 64 : 32;
-  const int tiles = lora_tiles(rows, n_adapters, tile);
-  int splits = ceil_div(512, tiles);
-  if (splits > most) splits = most;
-  return LoraPlan{tile, splits, many ? 1024 : 256};
+inline LoraPlan lora_plan(int rows, int n, int k, int rank, int n_adapters, int x_rows, bool y_f32) {
+  LoraPlan p{};
+  // Long runs take tiles of 32 rows, which read A and B half as often: 8192 rows
+  // of 5 adapters of 5120 x 5120, rank 64: 67 us against 90; 205 rows of each 22
+  // against 24.4, 51 of each 19 against 16.4. Above rank 64 such a tile leaves one
+  // wave a SIMD: 4096 rows at rank 128 67 us either way, 2048 55 against 51.
+  p.tile = rows >= 128 * (rank > 64 ? 4 : 1) * (int64_t)n_adapters ? 32 : 16;
+  const int tiles = lora_tiles(rows, n_adapters, p.tile), blocks = ceil_div(k, kKBlock);
+  // Ten blocks of k a part, for four waves: one row of 5120 in 8 parts 9.1 us, in
+  // 4 9.4, in 16 9.3; 64 rows of 17408 in 16 parts 14.4, in 8 15.7. Fewer where
+  // tiles fill the CUs (512 rows of rank 128: 4 parts 28.7, 8 33.7).
+  p.splits = blocks / 10 < ceil_div(256, tiles) ? blocks / 10 : ceil_div(256, tiles);
+  p.splits = p.splits < 1 ? 1 : p.splits > 16 ? 16 : p.splits;
+  // As many columns' shares as let all workgroups run at once, but for an eighth:
+  // `waves` a SIMD is what the second kernel's registers allow. 64 rows of 24
+  // adapters by 512 of 17408 columns 15.6 us, by 256 17.6; 4096 rows of rank 64 by
+  // 1280 of 5120 42, by 1024 49, by 2560 54.
+  const int waves = p.tile == 16 ? (rank <= 32 ? 4 : rank <= 64 ? 3 : 2) : rank <= 32 && !y_f32 ? 3 : rank <= 64 ? 2 : 1;
+  const int shares = 288 * waves / tiles < 1 ? 1 : 288 * waves / tiles;
+  p.columns = ceil_div(ceil_div(n, shares), 256) * 256;
+  // y larger than all L2s (4096 x 5120 bf16: 34 us against 38, 1024 x 5120 fp32,
+  // which stays in them, 23 against 20).
+  p.far = (int64_t)x_rows * n * (y_f32 ? 4 : 2) >= (int64_t)32 << 20;
+  return p;
+}
+
+// Workgroups of the second launch stay far inside 32 bits.
+inline bool lora_in_grid(int rows, int n, int n_adapters) {
+  return (int64_t)lora_tiles(rows, n_adapters, 16) * ceil_div(n, 256) <= (int64_t)1 << 28;
 }
 
 // The first product's sums, fp32 [splits][rows][rank].
 inline size_t lora_workspace(int rows, int n, int k, int rank, int n_adapters) {
-  return (size_t)lora_plan(rows, n, k, rank, n_adapters).splits * rows * rank * 4;
+  return (size_t)lora_plan(rows, n, k, rank, n_adapters, 0, false).splits * rows * rank * 4;
 }
 
 // ---- verification ------------------------------------------------------------------

@@ -98,7 +98,8 @@ class Case:
 @pytest.mark.parametrize("rows,n,k,rank,adapters", [
     (1, 1, 8, 8, 1), (1, 5120, 512, 16, 8), (2, 64, 64, 16, 2), (5, 65, 72, 8, 3), (16, 257, 200, 24, 5), (17, 300, 136, 32, 4),
     (40, 129, 1000, 40, 40), (64, 1000, 512, 64, 24), (63, 260, 264, 128, 3), (130, 190, 520, 72, 2), (300, 333, 200, 16, 3),
-    (700, 259, 136, 64, 2), (400, 1100, 72, 104, 1), (100, 70, 64, 8, 1024)])
+    (700, 259, 136, 64, 2), (400, 1100, 72, 104, 1), (100, 70, 64, 8, 1024), (530, 130, 72, 128, 1), (1100, 75, 64, 8, 2),
+    (1030, 66, 80, 24, 5)])
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 def test_against_the_oracle(q, dev, rows, n, k, rank, adapters, out):
     for mixed in (True, False):
@@ -115,8 +116,16 @@ def test_lengths_of_k(q, dev, k):
 
 @pytest.mark.parametrize("rows", [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 200])
 @pytest.mark.parametrize("rank", [16, 128])
-def test_one_adapter_for_all(q, dev, rows, rank):
+def test_one_adapter_for_all(q, dev, rows, rank):   # tiles of 16 rows, and of 32 from 128 (512) rows on
     c = Case(rng(rows, rank), rows, 100, 96, rank, 1, "f32", owner=np.zeros(rows), mixed=False)
+    c.holds(c.run(q, dev))
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("adapters", [3, 40])
+@pytest.mark.parametrize("rank,n", [(16, 18901), (40, 18896), (72, 18904)])
+def test_results_larger_than_the_caches(q, dev, out, adapters, rank, n):
+    c = Case(rng(n, adapters), 1800 if rank > 64 else 900, n, 64, rank, adapters, out)
     c.holds(c.run(q, dev))
 
 

@@ -154,7 +154,7 @@ def test_lora_workspaces():
                 # at most 16 parts of k, none without a block of 64
                 assert b % (rows * 64 * 4) == 0 and 1 <= b // (rows * 64 * 4) <= max(1, min(16, -(-k // 64))), (rows, k, e)
     # few rows: the parts of k, and so a row's bits, go by k alone
-    assert {L.qmm_lora_workspace(r, 5120, 5120, 64, e) // r for r in (1, 2, 7, 16) for e in (1, 3, 1024)} == {16 * 256}
+    assert {L.qmm_lora_workspace(r, 5120, 5120, 64, e) // r for r in (1, 2, 7, 16) for e in (1, 3, 1024)} == {8 * 256}
 
 
 def verify(p=X, qq=Z, ty=F32, tok=IDS, ln=LEN, u=U, acc=DW, out=Y, r=3, d=4, v=1000, ws=TMP, wn=1 << 30):
