@@ -11,7 +11,7 @@
 // h keeps its 24 bits through the matrix cores: cut into three bf16 values of
 // eight bits each, hi + mid + lo == h, three instructions for one. The products
 // are exact in fp32, so y loses what fp32 additions lose.
-#include "qmv_device.h"
+#include "rows_device.h"
 #include "rows_internal.h"
 #include "rows_layout.h"
 #include "../../include/qmm_rows.h"
@@ -23,14 +23,6 @@ typedef float v4f __attribute__((ext_vector_type(4)));
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-// LDS that a wave alone uses: its writes before, its lanes' reads of each other's
-// values behind. The machine keeps a wave's LDS accesses in order; this keeps the
-// compiler to it.
-__device__ __forceinline__ void in_order() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 constexpr v4f kZero4 = {0.0f, 0.0f, 0.0f, 0.0f};
 constexpr u4 kNone = {0, 0, 0, 0};
 
@@ -39,20 +31,6 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? l
 
 __device__ __forceinline__ v4f mma(u4 a, u4 b, v4f d) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), d, 0, 0, 0);
-}
-
-// Inclusive sum over the wave's lanes, by six additions of permuted operands.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ int add_from(int v) {
-  return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
-}
-__device__ __forceinline__ int wave_upto(int v) {
-  v = add_from<0x111, 0xF>(v);   // row_shr:1, within rows of 16 lanes
-  v = add_from<0x112, 0xF>(v);
-  v = add_from<0x114, 0xF>(v);
-  v = add_from<0x118, 0xF>(v);
-  v = add_from<0x142, 0xA>(v);   // lane 15 of rows 0 and 2 to the rows behind them
-  return add_from<0x143, 0xC>(v);   // lane 31 to rows 2 and 3
 }
 
 __device__ __forceinline__ void run_of(const LoraArgs &p, int e, int &begin, int &end) {

@@ -12,8 +12,6 @@
 namespace qmv {
 namespace {
 
-constexpr int kGroup = 8;   // choices whose loads are sent together
-
 // 16 bytes at the alignment A of an element or of a whole piece.
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u4_at4 __attribute__((ext_vector_type(4), aligned(4)));
@@ -35,11 +33,13 @@ struct Piece<2> {
 template <bool F32>
 constexpr int kValues = F32 ? 4 : 8;
 
-// Piece c of a row of `width` values; behind the end: zeros.
-template <bool F32, int A>
+// Piece c of a row of `width` values; behind the end: zeros. FAR (whole pieces):
+// past the caches.
+template <bool F32, int A, bool FAR = false>
 __device__ __forceinline__ u4 load_piece(const void *rows, size_t row, int c, int width) {
   constexpr int V = kValues<F32>;
   const char *at = static_cast<const char *>(rows) + (row * width + (size_t)c * V) * (F32 ? 4 : 2);
+  if constexpr (FAR) return __builtin_nontemporal_load(reinterpret_cast<const u4 *>(at));
   if (A == 16 || (c + 1) * V <= width) return *reinterpret_cast<const typename Piece<A>::type *>(at);
   u4 v = {0, 0, 0, 0};
 #pragma unroll
@@ -53,10 +53,14 @@ __device__ __forceinline__ u4 load_piece(const void *rows, size_t row, int c, in
   return v;
 }
 
-template <bool F32, int A>
+template <bool F32, int A, bool FAR = false>
 __device__ __forceinline__ void store_piece(void *rows, size_t row, int c, int width, u4 v) {
   constexpr int V = kValues<F32>;
   char *at = static_cast<char *>(rows) + (row * width + (size_t)c * V) * (F32 ? 4 : 2);
+  if constexpr (FAR) {
+    __builtin_nontemporal_store(v, reinterpret_cast<u4 *>(at));
+    return;
+  }
   if (A == 16 || (c + 1) * V <= width) {
     *reinterpret_cast<typename Piece<A>::type *>(at) = v;
     return;
@@ -93,10 +97,11 @@ __device__ __forceinline__ u4 pack(const float (&f)[kValues<F32>]) {
   return v;
 }
 
-// The places of choices j0 .. j0 + kGroup - 1 of token t; -1 where none is.
-__device__ __forceinline__ void load_places(const MoveArgs &p, int t, int j0, int (&at)[kGroup]) {
+// The places of choices j0 .. j0 + G - 1 of token t; -1 where none is.
+template <int G>
+__device__ __forceinline__ void load_places(const MoveArgs &p, int t, int j0, int (&at)[G]) {
 #pragma unroll
-  for (int j = 0; j < kGroup; ++j) {
+  for (int j = 0; j < G; ++j) {
     const int v = j0 + j < p.top_k ? p.places[(size_t)t * p.top_k + j0 + j] : -1;
     at[j] = (unsigned)v < (unsigned)p.rows ? v : -1;
   }
@@ -110,23 +115,24 @@ __device__ __forceinline__ bool own_piece(const MoveArgs &p, int shift, int piec
   return c < pieces;
 }
 
-template <bool F32, int A>
+template <bool F32, int A, bool FAR>
 __global__ __launch_bounds__(256) void rows_spread_kernel(const MoveArgs p, const int shift, const int pieces) {
   int t, step, c;
   if (!own_piece(p, shift, pieces, t, step, c)) return;
   for (; t < p.tokens; t += step) {
     const u4 v = load_piece<F32, A>(p.x, t, c, p.width);
-    for (int j0 = 0; j0 < p.top_k; j0 += kGroup) {
-      int at[kGroup];
+    for (int j0 = 0; j0 < p.top_k; j0 += 8) {
+      int at[8];
       load_places(p, t, j0, at);
 #pragma unroll
-      for (int j = 0; j < kGroup; ++j)
-        if (at[j] >= 0) store_piece<F32, A>(p.out, at[j], c, p.width, v);
+      for (int j = 0; j < 8; ++j)
+        if (at[j] >= 0) store_piece<F32, A, FAR>(p.out, at[j], c, p.width, v);
     }
   }
 }
 
-template <bool ZF32, bool YF32, int A>
+// The rows of G choices are sent for together.
+template <bool ZF32, bool YF32, int A, int G, bool FAR>
 __global__ __launch_bounds__(256) void rows_combine_kernel(const MoveArgs p, const int shift, const int pieces) {
   constexpr int V = kValues<ZF32>;
   int t, step, c;
@@ -135,24 +141,24 @@ __global__ __launch_bounds__(256) void rows_combine_kernel(const MoveArgs p, con
     float sum[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) sum[i] = 0.0f;
-    for (int j0 = 0; j0 < p.top_k && p.rows > 0; j0 += kGroup) {
-      int at[kGroup];
-      float w[kGroup];
-      u4 v[kGroup];
+    for (int j0 = 0; j0 < p.top_k && p.rows > 0; j0 += G) {
+      int at[G];
+      float w[G];
+      u4 v[G];
       load_places(p, t, j0, at);
 #pragma unroll
-      for (int j = 0; j < kGroup; ++j) {   // without a place: row 0 is read and not added
-        v[j] = load_piece<ZF32, A>(p.x, at[j] < 0 ? 0 : at[j], c, p.width);
+      for (int j = 0; j < G; ++j) {   // without a place: row 0 is read and not added
+        v[j] = load_piece<ZF32, A, FAR>(p.x, at[j] < 0 ? 0 : at[j], c, p.width);
         w[j] = p.w && j0 + j < p.top_k ? p.w[(size_t)t * p.top_k + j0 + j] : 1.0f;
       }
 #pragma unroll
-      for (int j = 0; j < kGroup; ++j)
+      for (int j = 0; j < G; ++j)
         if (at[j] >= 0)
 #pragma unroll
           for (int i = 0; i < V; ++i) sum[i] = __builtin_fmaf(w[j], value<ZF32>(v[j], i), sum[i]);
     }
     if constexpr (ZF32 == YF32) {
-      store_piece<YF32, A>(p.out, t, c, p.width, pack<YF32>(sum));
+      store_piece<YF32, A, FAR>(p.out, t, c, p.width, pack<YF32>(sum));
     } else if constexpr (YF32) {   // a piece of z is two of y
       const float lo[4] = {sum[0], sum[1], sum[2], sum[3]}, hi[4] = {sum[4], sum[5], sum[6], sum[7]};
       store_piece<true, A == 2 ? 4 : A>(p.out, t, 2 * c, p.width, pack<true>(lo));
@@ -173,58 +179,58 @@ __global__ __launch_bounds__(256) void rows_combine_kernel(const MoveArgs p, con
 }
 
 // LANES lanes a token (a wave, or the whole workgroup), which keep the dot
-// products of up to eight choices in registers and add them up at the end, in an
-// order that goes by the width alone.
-template <bool F32, int A, int LANES>
+// products of G choices in registers and add them up at the end, in an order that
+// goes by the width alone.
+template <bool F32, int A, int LANES, int G, bool FAR>
 __global__ __launch_bounds__(256) void rows_combine_grad_kernel(const MoveArgs p, const int pieces) {
   constexpr int V = kValues<F32>;
-  __shared__ float waves[4][kGroup];
+  __shared__ float waves[4][G];
   const int lane = (int)threadIdx.x & (LANES - 1), step = (int)(gridDim.x * 256) / LANES;
   for (int t = (int)(blockIdx.x * 256 + threadIdx.x) / LANES; t < p.tokens; t += step) {
-    for (int j0 = 0; j0 < p.top_k; j0 += kGroup) {
-      int at[kGroup];
-      float w[kGroup], dot[kGroup];
+    for (int j0 = 0; j0 < p.top_k; j0 += G) {
+      int at[G];
+      float w[G], dot[G];
       load_places(p, t, j0, at);
 #pragma unroll
-      for (int j = 0; j < kGroup; ++j) {
+      for (int j = 0; j < G; ++j) {
         w[j] = p.w && j0 + j < p.top_k ? p.w[(size_t)t * p.top_k + j0 + j] : 1.0f;
         dot[j] = 0.0f;
       }
       for (int c = lane; c < pieces && p.rows > 0; c += LANES) {
         const u4 dy = load_piece<F32, A>(p.x, t, c, p.width);
         if (p.z) {
-          u4 z[kGroup];
+          u4 z[G];
 #pragma unroll
-          for (int j = 0; j < kGroup; ++j) z[j] = load_piece<F32, A>(p.z, at[j] < 0 ? 0 : at[j], c, p.width);
+          for (int j = 0; j < G; ++j) z[j] = load_piece<F32, A, FAR>(p.z, at[j] < 0 ? 0 : at[j], c, p.width);
 #pragma unroll
-          for (int j = 0; j < kGroup; ++j)
+          for (int j = 0; j < G; ++j)
 #pragma unroll
             for (int i = 0; i < V; ++i) dot[j] = __builtin_fmaf(value<F32>(dy, i), value<F32>(z[j], i), dot[j]);
         }
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) {
+        for (int j = 0; j < G; ++j) {
           if (at[j] < 0) continue;
           float f[V];
 #pragma unroll
           for (int i = 0; i < V; ++i) f[i] = w[j] * value<F32>(dy, i);
-          store_piece<F32, A>(p.out, at[j], c, p.width, pack<F32>(f));
+          store_piece<F32, A, FAR>(p.out, at[j], c, p.width, pack<F32>(f));
         }
       }
       if (!p.dw) continue;
 #pragma unroll
-      for (int j = 0; j < kGroup; ++j) dot[j] = group_sum<64>(dot[j]);
+      for (int j = 0; j < G; ++j) dot[j] = group_sum<64>(dot[j]);
       if constexpr (LANES == 256) {
         __syncthreads();
         if ((threadIdx.x & 63) == 0)
 #pragma unroll
-          for (int j = 0; j < kGroup; ++j) waves[threadIdx.x >> 6][j] = dot[j];
+          for (int j = 0; j < G; ++j) waves[threadIdx.x >> 6][j] = dot[j];
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) dot[j] = (waves[0][j] + waves[1][j]) + (waves[2][j] + waves[3][j]);
+        for (int j = 0; j < G; ++j) dot[j] = (waves[0][j] + waves[1][j]) + (waves[2][j] + waves[3][j]);
       }
       if (lane == 0)
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j)
+        for (int j = 0; j < G; ++j)
           if (j0 + j < p.top_k) p.dw[(size_t)t * p.top_k + j0 + j] = at[j] < 0 ? 0.0f : dot[j];
     }
   }
@@ -252,8 +258,10 @@ unsigned token_groups(int tokens, int lanes) {
   return g < kMostGroups ? g : kMostGroups;
 }
 
+int pieces_of(const MoveArgs &a) { return rows::ceil_div(a.width, a.in_f32 ? 4 : 8); }
+
 int launch_move(const char *name, void (*kernel)(const MoveArgs, const int, const int), const MoveArgs &a, hipStream_t s) {
-  const int pieces = rows::ceil_div(a.width, a.in_f32 ? 4 : 8), shift = lanes_shift(pieces);
+  const int pieces = pieces_of(a), shift = lanes_shift(pieces);
   return launch_kernel(name, kernel, dim3(token_groups(a.tokens, 1 << shift), (unsigned)rows::ceil_div(pieces, 1 << shift)),
                        dim3(256), 0, s, a, shift, pieces);
 }
@@ -261,43 +269,65 @@ int launch_move(const char *name, void (*kernel)(const MoveArgs, const int, cons
 // Rows whose every piece is whole and 16-byte aligned.
 bool whole(const MoveArgs &a) { return a.width % (a.in_f32 ? 4 : 8) == 0; }
 
-template <bool F32, int A>
-int launch_grad(const MoveArgs &a, hipStream_t s) {
-  const int pieces = rows::ceil_div(a.width, kValues<F32>);
-  const bool wide = a.tokens < 4096 && pieces > 64;
-  return wide ? launch_kernel("rows_combine_grad_kernel", rows_combine_grad_kernel<F32, A, 256>,
-                              dim3(token_groups(a.tokens, 256)), dim3(256), 0, s, a, pieces)
-              : launch_kernel("rows_combine_grad_kernel", rows_combine_grad_kernel<F32, A, 64>,
-                              dim3(token_groups(a.tokens, 64)), dim3(256), 0, s, a, pieces);
+bool far(const MoveArgs &a) {
+  return rows::past_caches((int64_t)a.tokens * a.top_k < a.rows ? a.tokens * a.top_k : a.rows, a.width, a.in_f32);
+}
+
+template <bool F32>
+int spread(const MoveArgs &a, hipStream_t s) {
+  return launch_move("rows_spread_kernel",
+                     !whole(a) ? rows_spread_kernel<F32, F32 ? 4 : 2, false>
+                     : far(a)  ? rows_spread_kernel<F32, 16, true>
+                               : rows_spread_kernel<F32, 16, false>,
+                     a, s);
+}
+
+template <bool ZF32, bool YF32, int G>
+int combine(const MoveArgs &a, hipStream_t s) {
+  return launch_move("rows_combine_kernel",
+                     !whole(a) ? rows_combine_kernel<ZF32, YF32, ZF32 ? 4 : 2, G, false>
+                     : far(a)  ? rows_combine_kernel<ZF32, YF32, 16, G, true>
+                               : rows_combine_kernel<ZF32, YF32, 16, G, false>,
+                     a, s);
+}
+
+template <int G>
+int combine_of(const MoveArgs &a, hipStream_t s) {
+  if (a.in_f32) return a.out_f32 ? combine<true, true, G>(a, s) : combine<true, false, G>(a, s);
+  return a.out_f32 ? combine<false, true, G>(a, s) : combine<false, false, G>(a, s);
+}
+
+template <bool F32, int LANES, int G>
+int grad(const MoveArgs &a, hipStream_t s) {
+  return launch_kernel("rows_combine_grad_kernel",
+                       !whole(a) ? rows_combine_grad_kernel<F32, F32 ? 4 : 2, LANES, G, false>
+                       : far(a)  ? rows_combine_grad_kernel<F32, 16, LANES, G, true>
+                                 : rows_combine_grad_kernel<F32, 16, LANES, G, false>,
+                       dim3(token_groups(a.tokens, LANES)), dim3(256), 0, s, a, pieces_of(a));
+}
+
+template <int G>
+int grad_of(const MoveArgs &a, hipStream_t s) {
+  const bool wide = pieces_of(a) > 64;
+  if (a.in_f32) return wide ? grad<true, 256, G>(a, s) : grad<true, 64, G>(a, s);
+  return wide ? grad<false, 256, G>(a, s) : grad<false, 64, G>(a, s);
 }
 
 }  // namespace
 
 int launch_rows_spread(const MoveArgs &a, void *stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const char *name = "rows_spread_kernel";
-  if (a.in_f32)
-    return whole(a) ? launch_move(name, rows_spread_kernel<true, 16>, a, s) : launch_move(name, rows_spread_kernel<true, 4>, a, s);
-  return whole(a) ? launch_move(name, rows_spread_kernel<false, 16>, a, s) : launch_move(name, rows_spread_kernel<false, 2>, a, s);
+  return a.in_f32 ? spread<true>(a, s) : spread<false>(a, s);
 }
 
 int launch_rows_combine(const MoveArgs &a, void *stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const char *name = "rows_combine_kernel";
-  const bool w = whole(a);
-  if (a.in_f32 && a.out_f32)
-    return w ? launch_move(name, rows_combine_kernel<true, true, 16>, a, s) : launch_move(name, rows_combine_kernel<true, true, 4>, a, s);
-  if (a.in_f32)
-    return w ? launch_move(name, rows_combine_kernel<true, false, 16>, a, s) : launch_move(name, rows_combine_kernel<true, false, 4>, a, s);
-  if (a.out_f32)
-    return w ? launch_move(name, rows_combine_kernel<false, true, 16>, a, s) : launch_move(name, rows_combine_kernel<false, true, 2>, a, s);
-  return w ? launch_move(name, rows_combine_kernel<false, false, 16>, a, s) : launch_move(name, rows_combine_kernel<false, false, 2>, a, s);
+  return a.top_k <= 2 ? combine_of<2>(a, s) : a.top_k <= 4 ? combine_of<4>(a, s) : combine_of<8>(a, s);
 }
 
 int launch_rows_combine_grad(const MoveArgs &a, void *stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
-  if (a.in_f32) return whole(a) ? launch_grad<true, 16>(a, s) : launch_grad<true, 4>(a, s);
-  return whole(a) ? launch_grad<false, 16>(a, s) : launch_grad<false, 2>(a, s);
+  return a.top_k <= 2 ? grad_of<2>(a, s) : a.top_k <= 4 ? grad_of<4>(a, s) : grad_of<8>(a, s);
 }
 
 }  // namespace qmv

@@ -95,7 +95,8 @@ def sort_into_guards(q, dev, ids, experts, ws=None):
 @pytest.mark.parametrize("tokens,top_k,experts", [
     (1, 1, 1), (1, 8, 128), (4, 8, 128), (3, 2, 3), (64, 1, 5), (65, 1, 64), (21, 3, 65), (128, 32, 1024), (512, 8, 128),
     (4096, 1, 1), (1365, 3, 60), (513, 8, 128), (4097, 1, 2), (1025, 4, 1), (1024, 5, 1024), (2500, 2, 255), (2100, 2, 256),
-    (2100, 2, 257), (6000, 8, 17)])
+    (2100, 2, 257), (6000, 8, 17), (16384, 1, 7), (16385, 1, 2), (3300, 5, 1024), (17000, 1, 1),
+    (9000, 2, 257), (20, 32, 1024), (640, 1, 1024)])
 @pytest.mark.parametrize("dropped", [0.0, 0.3])
 def test_sort(q, dev, tokens, top_k, experts, dropped):
     g = rng(tokens, top_k, experts, int(dropped * 10))
@@ -128,7 +129,7 @@ def test_sort_of_many_choices_and_extreme_ids(q, dev):
 def test_sort_without_tokens_or_some_outputs(q, dev):
     off, idx, pl = q.qmm_rows_sort(torch.empty((0, 4), dtype=torch.int32, device=dev), 3)
     assert host(off).tolist() == [0, 0, 0, 0] and idx.shape == (0,) and pl.shape == (0, 4)
-    for tokens in (50, 5000):                                  # the C entry takes null for either
+    for tokens in (50, 5000, 10000):                           # the C entry takes null for either
         ids = choices(rng(tokens), tokens, 2, 9)
         want = np_sort(ids, 9)
         d, ws = up(ids, dev), torch.empty(max(1, q.qmm_rows_sort_workspace(tokens, 2, 9)), dtype=torch.uint8, device=dev)
@@ -286,6 +287,27 @@ def test_places_outside_are_passed_over(q, dev):
     assert torch.equal(y[0], x[0]) and torch.equal(y[2], x[2]) and bool((y[1] == 0).all())
 
 
+@pytest.mark.parametrize("top_k,h", [(2, 16384), (4, 8192), (9, 4096)])
+def test_rows_larger_than_the_caches(q, dev, top_k, h):
+    # from 64 MiB of rows on they go past the caches: bf16, and the same in fp32, against sums of whole numbers
+    g = rng(9, top_k)
+    tokens = -(-(64 << 20) // (top_k * h * 2)) + 1
+    places = np_sort(choices(g, tokens, top_k, 50, 0.1), 50)[2].astype(np.int32)
+    x = torch.from_numpy(g.integers(-8, 9, (tokens, h)).astype(np.float32)).to(dev)
+    w = torch.from_numpy(g.integers(-4, 5, (tokens, top_k)).astype(np.float32)).to(dev)
+    at = up(places, dev)
+    held = (at >= 0).float()
+    for kind in (torch.bfloat16, torch.float32):
+        z = q.qmm_rows_spread(x.to(kind), at)
+        ids = torch.where(at < 0, 0, at).long()
+        assert torch.equal(z[ids] * held[:, :, None].to(kind), x.to(kind)[:, None] * held[:, :, None].to(kind))
+        y = q.qmm_rows_combine(z, at, w)
+        assert torch.equal(y, x * (w * held).sum(1, keepdim=True))         # below 2^24: exact
+        dz, dw = q.qmm_rows_combine_grad(x.to(kind), z, at, w)
+        assert torch.equal(dz[ids] * held[:, :, None].to(kind), (x[:, None] * (w * held)[:, :, None]).to(kind))
+        assert torch.equal(dw, (x * x).sum(1, keepdim=True) * held)        # at most 64 * 2^14
+
+
 def test_rows_past_4_gib(q, dev):
     # 2^21 + 5 rows of 1024 fp32 values: the last rows' addresses pass 2^32 bytes, and 2^31 values
     rows, h = (1 << 21) + 5, 1024
@@ -304,11 +326,12 @@ def test_rows_past_4_gib(q, dev):
 
 def test_another_stream_and_a_graph(q, dev):
     g = rng(6)
-    ids = [choices(g, 600, 8, 128, 0.1) for _ in range(4)]
-    x, x64 = values(g, "bf16", 600, 256)
-    w = g.random((600, 8)).astype(np.float32)
+    tokens = 2100                                              # enough for the sort to need its workspace
+    ids = [choices(g, tokens, 8, 128, 0.1) for _ in range(4)]
+    x, x64 = values(g, "bf16", tokens, 256)
+    w = g.random((tokens, 8)).astype(np.float32)
     xd, wd, idsd = x.to(dev), up(w, dev), up(ids[0], dev)
-    ws = torch.empty(q.qmm_rows_sort_workspace(600, 8, 128), dtype=torch.uint8, device=dev)
+    ws = torch.empty(q.qmm_rows_sort_workspace(tokens, 8, 128), dtype=torch.uint8, device=dev)
     state = {}
 
     def layer():

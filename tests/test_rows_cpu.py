@@ -55,10 +55,10 @@ def test_sort_refusals():
 
 
 def test_sort_workspaces():
-    assert L.qmm_rows_sort_workspace(4, 8, 128) == 0 and L.qmm_rows_sort_workspace(512, 8, 1024) == 0
+    assert L.qmm_rows_sort_workspace(4, 8, 128) == 0 and L.qmm_rows_sort_workspace(2048, 8, 1024) == 0
     for bad in ((-1, 8, 128), (4, 0, 128), (4, 33, 128), (4, 8, 0), (4, 8, 1025), (1 << 22, 8, 128)):
         assert L.qmm_rows_sort_workspace(*bad) == 0, bad
-    for t in (513, 1000, 8192, 1 << 20, 1 << 21):
+    for t in (2049, 2500, 8192, 1 << 20, 1 << 21):
         b = L.qmm_rows_sort_workspace(t, 8, 128)
         assert 0 < b <= 256 * 128 * 4 and b % 512 == 0, t
     assert q.qmm_rows_sort_workspace((1 << 32) + 4, 8, 128) == 0
