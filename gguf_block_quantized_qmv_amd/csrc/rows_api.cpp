@@ -248,7 +248,7 @@ int qmv_verify_drafts(const void *p, const void *q, int type, const int32_t *tok
   v.u = u;
   v.accepted = accepted;
   v.out = out;
-  v.sums = static_cast<double *>(ws);
+  v.sums = need ? static_cast<double *>(ws) : nullptr;
   v.f32 = type == QMM_F32;
   v.requests = requests;
   v.drafts = drafts;

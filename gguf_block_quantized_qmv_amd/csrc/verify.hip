@@ -2,27 +2,28 @@
 // them, from given random numbers; gfx950.
 //
 // Of the probabilities only one row of p and of q a request matters beyond the
-// drafts' own entries. The first launch cuts that row into chunks of 4096 for a
-// workgroup each and leaves two sums by chunk: the weights max(p - q, 0) and p
-// alone. The second adds up a request's chunks, finds the one in which the
-// running sum passes u times the whole, and the token in it.
+// drafts' own entries. It is cut into chunks of 1024 tokens for a wave each, which
+// leaves two sums by chunk: the weights max(p - q, 0) and p alone. One wave then
+// adds up a request's chunks, finds the one in which the running sum passes u times
+// the whole, and the token in it. Either a workgroup does all of that for a
+// request, or a first launch spreads the chunks over the CUs and a second picks.
 //
 // Sums are fp64: over a vocabulary of 10^5 an fp32 sum would move the borders
 // between tokens by more than a rare token's own weight. A draft's test takes
 // the product u * q in fp64, where it is exact.
-#include <limits.h>
+#include <float.h>
 
-#include "qmv_device.h"
+#include "rows_device.h"
 #include "rows_internal.h"
 #include "rows_layout.h"
 
 namespace qmv {
 namespace {
 
-constexpr int kPer = rows::kVerifyChunk / 256;   // tokens a thread
+constexpr int kPer = rows::kVerifyChunk / 64;   // tokens a lane
 
-// kPer values of one row from memory. Thread i holds, for each vector h, the
-// values (h * 256 + i) * V .. + V - 1 of the chunk; behind the end: zeros.
+// A chunk of one row from memory. Lane i holds, for each vector h, the values
+// (h * 64 + i) * V .. + V - 1 of it; behind the end: zeros.
 template <bool F32>
 struct Values {
   static constexpr int V = F32 ? 4 : 8, H = kPer / V;
@@ -32,7 +33,7 @@ struct Values {
     typedef uint32_t Vec __attribute__((ext_vector_type(4), aligned(2)));   // the start of a row is any element's
 #pragma unroll
     for (int h = 0; h < H; ++h) {
-      const int at = first + (h * 256 + (int)threadIdx.x) * V;
+      const int at = first + (h * 64 + ((int)threadIdx.x & 63)) * V;
       if (at + V <= vocab) {
         const Vec u = *reinterpret_cast<const Vec *>(static_cast<const char *>(row) + (size_t)at * (F32 ? 4 : 2));
 #pragma unroll
@@ -58,8 +59,13 @@ __device__ __forceinline__ float entry(const void *row, int f32, int i) {
   return f32 ? static_cast<const float *>(row)[i] : bf16_bits_to_f32(static_cast<const uint16_t *>(row)[i]);
 }
 
-// A weight: what is negative or not finite counts as zero.
-__device__ __forceinline__ double weight(double d) { return d > 0.0 && d <= 1.7976931348623157e308 ? d : 0.0; }
+// p - q where that is a weight: what is negative or not finite counts as zero.
+// Tested in fp64: with the tests in fp32 the sums' kernel takes 87 registers instead
+// of 52, and 128 rows of 131072 bf16 26 us instead of 23.
+__device__ __forceinline__ double weight(float p, float q) {
+  const double d = (double)p - (double)q;
+  return d > 0.0 && d <= DBL_MAX ? d : 0.0;
+}
 
 __device__ __forceinline__ const void *row_of(const void *p, int f32, size_t row, int vocab) {
   return static_cast<const char *>(p) + row * vocab * (f32 ? 4 : 2);
@@ -98,202 +104,193 @@ __device__ __forceinline__ Outcome judge(const VerifyArgs &a, int r) {
   return Outcome{n, __builtin_amdgcn_readlane(token, n), n < length};
 }
 
-// The weights of a chunk, and p alone, by which a refused draft without any picks.
+// Sums over a wave's lanes up to and with each lane, and its last lane's value.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double add_from(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)u, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, ROWS, 0xF, false);
+  return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double wave_upto(double v) {
+  v = add_from<0x111, 0xF>(v);   // as the whole numbers' sum in rows_device.h
+  v = add_from<0x112, 0xF>(v);
+  v = add_from<0x114, 0xF>(v);
+  v = add_from<0x118, 0xF>(v);
+  v = add_from<0x142, 0xA>(v);
+  return add_from<0x143, 0xC>(v);
+}
+__device__ __forceinline__ double of_lane(double v, int lane) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)u, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(u >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+// p and q of a chunk: the weights, and p's own, by which a refused draft without
+// any weight picks.
 template <bool F32>
-__device__ __forceinline__ void weights(const VerifyArgs &a, int r, const Outcome &o, int first, double (&rest)[kPer],
-                                        double (&left)[kPer]) {
-  constexpr int V = Values<F32>::V, H = Values<F32>::H;
+struct Chunk {
+  static constexpr int V = Values<F32>::V, H = Values<F32>::H;
   Values<F32> p, q;
-  p.load(row_of(a.p, F32, (size_t)r * (a.drafts + 1) + o.accepted, a.vocab), first, a.vocab);
-  const bool drafted = o.refused && a.q;
-  if (drafted) q.load(row_of(a.q, F32, (size_t)r * a.drafts + o.accepted, a.vocab), first, a.vocab);
+  int first, zero;   // zero: a token without q that was refused
+
+  __device__ __forceinline__ Chunk(const VerifyArgs &a, int r, const Outcome &o, int chunk) {
+    first = chunk * rows::kVerifyChunk;
+    zero = o.refused && !a.q ? o.token : -1;
+    p.load(row_of(a.p, F32, (size_t)r * (a.drafts + 1) + o.accepted, a.vocab), first, a.vocab);
+    if (o.refused && a.q) {
+      q.load(row_of(a.q, F32, (size_t)r * a.drafts + o.accepted, a.vocab), first, a.vocab);
+    } else {
 #pragma unroll
-  for (int h = 0; h < H; ++h)
+      for (int h = 0; h < H; ++h)
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const double v = (double)p.v[h][i];
-      left[h * V + i] = weight(v);
-      double d = v;
-      if (drafted) d = v - (double)q.v[h][i];
-      else if (o.refused && first + (h * 256 + (int)threadIdx.x) * V + i == o.token) d = 0.0;
-      rest[h * V + i] = weight(d);
+        for (int i = 0; i < V; ++i) q.v[h][i] = 0.0f;
     }
-}
+  }
+  __device__ __forceinline__ int token(int h, int i) const { return first + (h * 64 + ((int)threadIdx.x & 63)) * V + i; }
+  __device__ __forceinline__ double left(int h, int i) const { return weight(p.v[h][i], 0.0f); }
+  __device__ __forceinline__ double rest(int h, int i) const {
+    return token(h, i) == zero ? 0.0 : weight(p.v[h][i], q.v[h][i]);
+  }
+};
 
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-  return v;
-}
-
+// A chunk's two sums, by one wave.
 template <bool F32>
-__global__ __launch_bounds__(256) void verify_sums_kernel(const VerifyArgs a, const int chunks) {
-  __shared__ double waves[4][2];
-  const int r = (int)blockIdx.y, chunk = (int)blockIdx.x;
-  const Outcome o = judge(a, r);
-  if (chunk == 0 && threadIdx.x == 0) a.accepted[r] = o.accepted;
-  double rest[kPer], left[kPer], s = 0.0, t = 0.0;
-  weights<F32>(a, r, o, chunk * rows::kVerifyChunk, rest, left);
+__device__ __forceinline__ void sum_chunk(const VerifyArgs &a, int r, const Outcome &o, int chunk, double *sums) {
+  const Chunk<F32> c(a, r, o, chunk);
+  double s = 0.0, t = 0.0;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    s += rest[i];
-    t += left[i];
+  for (int h = 0; h < c.H; ++h)
+#pragma unroll
+    for (int i = 0; i < c.V; ++i) {
+      s += c.rest(h, i);
+      t += c.left(h, i);
+    }
+  s = wave_upto(s);
+  t = wave_upto(t);
+  if ((threadIdx.x & 63) == 63) {
+    sums[chunk * 2] = s;
+    sums[chunk * 2 + 1] = t;
   }
-  s = wave_sum(s);
-  t = wave_sum(t);
-  if ((threadIdx.x & 63) == 0) {
-    waves[threadIdx.x >> 6][0] = s;
-    waves[threadIdx.x >> 6][1] = t;
-  }
-  __syncthreads();
-  if (threadIdx.x < 2)
-    a.sums[((size_t)r * chunks + chunk) * 2 + threadIdx.x] =
-        (waves[0][threadIdx.x] + waves[1][threadIdx.x]) + (waves[2][threadIdx.x] + waves[3][threadIdx.x]);
 }
 
-// Inclusive sum over the wave.
-__device__ __forceinline__ double wave_scan(double v) {
+// The lanes that hold something, in the order of what they hold: the first and the last.
+__device__ __forceinline__ int first_lane(uint64_t b) { return __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)b) - 1); }
+__device__ __forceinline__ int last_lane(uint64_t b) { return __builtin_amdgcn_readfirstlane(63 - __clzll((long long)b)); }
+
+// The token that follows, and the request's row of `out`, by one wave.
+template <bool F32>
+__device__ __forceinline__ void pick(const VerifyArgs &a, int r, const Outcome &o, const float u, const double *sums,
+                                     const int chunks) {
   const int lane = (int)threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const double o = __shfl_up(v, d);
-    if (lane >= d) v += o;
+  const int per = rows::ceil_div(chunks, 64), c0 = lane * per;   // neighbouring chunks a lane
+  double own[2] = {0.0, 0.0}, upto[2];
+  for (int c = c0; c < c0 + per && c < chunks; ++c) {
+    own[0] += sums[c * 2];
+    own[1] += sums[c * 2 + 1];
   }
-  return v;
-}
-
-// Least of the workgroup's values.
-__device__ __forceinline__ int least(int v, int *waves) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int o = __shfl_xor(v, d);
-    v = o < v ? o : v;
-  }
-  __syncthreads();   // the last reads of `waves`
-  if ((threadIdx.x & 63) == 0) waves[threadIdx.x >> 6] = v;
-  __syncthreads();
-  const int a = waves[0] < waves[1] ? waves[0] : waves[1], b = waves[2] < waves[3] ? waves[2] : waves[3];
-  return a < b ? a : b;
-}
-
-template <bool F32>
-__global__ __launch_bounds__(256) void verify_pick_kernel(const VerifyArgs a, const int chunks) {
-  constexpr int V = Values<F32>::V, H = Values<F32>::H;
-  __shared__ double sums[2][4], runs[H][4], found_base;
-  __shared__ int waves[4];
-  const int r = (int)blockIdx.x, tid = (int)threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  Outcome o;
-  o.accepted = a.accepted[r];
-  o.refused = o.accepted < drafts_of(a, r);
-  o.token = o.refused ? a.tokens[(size_t)r * a.drafts + o.accepted] : -1;
-  const float u = a.u[(size_t)r * (a.drafts + 1) + a.drafts];
-
-  // every thread's neighbouring chunks, both sums
-  const int per = rows::ceil_div(chunks, 256), c0 = tid * per;
-  const double *sum = a.sums + (size_t)r * chunks * 2;
-  double upto[2] = {0.0, 0.0}, own[2];
-  for (int c = c0; c < c0 + per && c < chunks; ++c)
-#pragma unroll
-    for (int k = 0; k < 2; ++k) upto[k] += sum[c * 2 + k];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    own[k] = upto[k];
-    upto[k] = wave_scan(upto[k]);
-    if (lane == 63) sums[k][wave] = upto[k];
-  }
-  __syncthreads();
-  double all[2], before[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    double s = 0.0;
-    before[k] = 0.0;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      if (w == wave) before[k] = s;
-      s += sums[k][w];
-    }
-    all[k] = s;
-    before[k] += upto[k] - own[k];
-  }
-  const int kind = all[0] > 0.0 ? 0 : 1;
-  const double total = kind ? all[1] : all[0], target = (double)u * total;
+  upto[0] = wave_upto(own[0]);
+  upto[1] = wave_upto(own[1]);
+  const int kind = of_lane(upto[0], 63) > 0.0 ? 0 : 1;   // without a weight: p's own
+  const double total = of_lane(kind ? upto[1] : upto[0], 63), target = (double)u * total;
   int token = -1;
   if (total > 0.0) {
     // the first chunk whose running sum lies above the target, else the last with a weight
-    int first = INT_MAX, last = INT_MAX;   // last: negated, so that the least is the last
-    double run = kind ? before[1] : before[0], base = 0.0, base_last = 0.0;
+    int first = -1, last = -1;
+    double run = kind ? upto[1] - own[1] : upto[0] - own[0], base = 0.0, base_last = 0.0;
     for (int c = c0; c < c0 + per && c < chunks; ++c) {
-      const double s = sum[c * 2 + kind];
+      const double s = sums[c * 2 + kind];
       if (s > 0.0) {
-        last = -c;
+        last = c;
         base_last = run;
-        if (first == INT_MAX && run + s > target) {
+        if (first < 0 && run + s > target) {
           first = c;
           base = run;
         }
       }
       run += s;
     }
-    int chunk = least(first, waves);
-    if (chunk == INT_MAX) {
-      const int l = least(last, waves);
-      chunk = -l;
-      if (last == l) found_base = base_last;
-    } else if (first == chunk) {
-      found_base = base;
-    }
-    __syncthreads();
-    double rest[kPer], left[kPer], part[H];
-    weights<F32>(a, r, o, chunk * rows::kVerifyChunk, rest, left);
+    const uint64_t above = __ballot(first >= 0);
+    const int of = above ? first_lane(above) : last_lane(__ballot(last >= 0));
+    double at = of_lane(above ? base : base_last, of);
+    const Chunk<F32> c(a, r, o, __builtin_amdgcn_readlane(above ? first : last, of));
+    // the same for its tokens, vector by vector
+    int end = -1;
 #pragma unroll
-    for (int h = 0; h < H; ++h) {
-      double s = 0.0;
+    for (int h = 0; h < c.H; ++h) {
+      double v[c.V], s = 0.0;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        if (kind) rest[h * V + i] = left[h * V + i];
-        s += rest[h * V + i];
+      for (int i = 0; i < c.V; ++i) {
+        v[i] = kind ? c.left(h, i) : c.rest(h, i);
+        s += v[i];
       }
-      part[h] = wave_scan(s);
-      if (lane == 63) runs[h][wave] = part[h];
-      part[h] -= s;
-    }
-    __syncthreads();
-    double at = found_base;
-    first = last = INT_MAX;
+      const double with = wave_upto(s);
+      double here = at + (with - s);
+      at += of_lane(with, 63);
+      int t = -1, e = -1;
 #pragma unroll
-    for (int h = 0; h < H; ++h)
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        if (w == wave) {
-          double here = at + part[h];
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            const double v = rest[h * V + i];
-            here += v;
-            const int t = chunk * rows::kVerifyChunk + (h * 256 + tid) * V + i;
-            if (v > 0.0) {
-              last = -t;
-              if (first == INT_MAX && here > target) first = t;
-            }
-          }
+      for (int i = 0; i < c.V; ++i) {
+        here += v[i];
+        if (v[i] > 0.0) {
+          e = c.token(h, i);
+          if (t < 0 && here > target) t = e;
         }
-        at += runs[h][w];
       }
-    token = least(first, waves);
-    if (token == INT_MAX) token = -least(last, waves);
+      const uint64_t up = __ballot(t >= 0), some = __ballot(e >= 0);
+      if (up && token < 0) token = __builtin_amdgcn_readlane(t, first_lane(up));
+      if (some) end = __builtin_amdgcn_readlane(e, last_lane(some));
+    }
+    if (token < 0) token = end;
   }
-  if (tid <= a.drafts)
-    a.out[(size_t)r * (a.drafts + 1) + tid] =
-        tid < o.accepted ? a.tokens[(size_t)r * a.drafts + tid] : tid == o.accepted ? token : -1;
+  if (lane <= a.drafts)
+    a.out[(size_t)r * (a.drafts + 1) + lane] =
+        lane < o.accepted ? a.tokens[(size_t)r * a.drafts + lane] : lane == o.accepted ? token : -1;
+}
+
+template <bool F32>
+__global__ __launch_bounds__(256) void verify_sums_kernel(const VerifyArgs a, const int chunks) {
+  const int r = (int)blockIdx.y, chunk = (int)blockIdx.x * 4 + ((int)threadIdx.x >> 6);
+  if (chunk >= chunks) return;
+  const Outcome o = judge(a, r);
+  if (chunk == 0 && (threadIdx.x & 63) == 0) a.accepted[r] = o.accepted;
+  sum_chunk<F32>(a, r, o, chunk, a.sums + (size_t)r * chunks * 2);
+}
+
+template <bool F32>
+__global__ __launch_bounds__(64) void verify_pick_kernel(const VerifyArgs a, const int chunks) {
+  const int r = (int)blockIdx.x;
+  Outcome o;
+  o.accepted = a.accepted[r];
+  o.refused = o.accepted < drafts_of(a, r);
+  o.token = o.refused ? a.tokens[(size_t)r * a.drafts + o.accepted] : -1;
+  pick<F32>(a, r, o, a.u[(size_t)r * (a.drafts + 1) + a.drafts], a.sums + (size_t)r * chunks * 2, chunks);
+}
+
+// Both for one request in a workgroup of 16 waves.
+template <bool F32>
+__global__ __launch_bounds__(1024) void verify_whole_kernel(const VerifyArgs a, const int chunks) {
+  extern __shared__ double sums[];
+  const int r = (int)blockIdx.x, wave = (int)threadIdx.x >> 6;
+  const float u = a.u[(size_t)r * (a.drafts + 1) + a.drafts];
+  const Outcome o = judge(a, r);
+  for (int c = wave; c < chunks; c += 16) sum_chunk<F32>(a, r, o, c, sums);
+  __syncthreads();
+  if (wave) return;
+  if (threadIdx.x == 0) a.accepted[r] = o.accepted;
+  pick<F32>(a, r, o, u, sums, chunks);
 }
 
 template <bool F32>
 int launch(const VerifyArgs &a, hipStream_t s) {
   const int chunks = rows::ceil_div(a.vocab, rows::kVerifyChunk);
-  const int rc = launch_kernel("verify_sums_kernel", verify_sums_kernel<F32>, dim3((unsigned)chunks, (unsigned)a.requests),
-                               dim3(256), 0, s, a, chunks);
+  if (!a.sums)
+    return launch_kernel("verify_whole_kernel", verify_whole_kernel<F32>, dim3((unsigned)a.requests), dim3(1024),
+                         (size_t)chunks * 16, s, a, chunks);
+  const int rc = launch_kernel("verify_sums_kernel", verify_sums_kernel<F32>,
+                               dim3((unsigned)rows::ceil_div(chunks, 4), (unsigned)a.requests), dim3(256), 0, s, a, chunks);
   if (rc) return rc;
-  return launch_kernel("verify_pick_kernel", verify_pick_kernel<F32>, dim3((unsigned)a.requests), dim3(256), 0, s, a, chunks);
+  return launch_kernel("verify_pick_kernel", verify_pick_kernel<F32>, dim3((unsigned)a.requests), dim3(64), 0, s, a, chunks);
 }
 
 }  // namespace

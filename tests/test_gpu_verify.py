@@ -75,7 +75,8 @@ def wanted(p, qq, tokens, lengths, u):
 
 
 @pytest.mark.parametrize("requests,drafts,vocab", [(1, 3, 32768), (1, 1, 1), (7, 3, 2), (5, 4, 1000), (3, 2, 4095), (3, 2, 4096),
-                                                   (3, 2, 4097), (40, 3, 5003), (2, 32, 777), (6, 0, 9001), (2, 8, 50001)])
+                                                   (3, 2, 4097), (40, 3, 5003), (2, 32, 777), (6, 0, 9001), (2, 8, 50001),
+                                                   (3, 3, 16384), (3, 3, 16385), (9, 2, 17403), (1, 2, 131075)])
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("sampled", [True, False])
 def test_against_the_oracle(q, dev, requests, drafts, vocab, kind, sampled):
@@ -85,7 +86,8 @@ def test_against_the_oracle(q, dev, requests, drafts, vocab, kind, sampled):
         assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
 
 
-def test_every_border_of_small_sums(q, dev):
+@pytest.mark.parametrize("stride", [1, 97])
+def test_every_border_of_small_sums(q, dev, stride):
     # weights of few bits: every sum is exact, and u stands on, just below and just above each border
     g = rng(1)
     w = g.integers(0, 4, 300) / 1024
@@ -98,19 +100,20 @@ def test_every_border_of_small_sums(q, dev):
     us = np.unique(np.concatenate([run / total, np.nextafter((run / total).astype(np.float32), np.float32(0)),
                                    np.nextafter((run / total).astype(np.float32), np.float32(2))]).astype(np.float32))
     us = us[us < 1]
-    p = torch.from_numpy(np.tile(w, (len(us), 1, 1))).float()
+    p = torch.zeros((len(us), 1, 300 * stride))
+    p[:, :, ::stride] = torch.from_numpy(w).float()            # side by side, and spread over chunks
     c = (p, None, np.zeros((len(us), 0), np.int32), None, us[:, None])
     got, want = call(q, dev, *c), wanted(*c)
     assert np.array_equal(got[1], want[1]) and len(np.unique(got[1])) > 150
 
 
-def test_random_numbers_at_and_outside_their_ends(q, dev):
-    v = 9000
+@pytest.mark.parametrize("v", [9000, 70000])
+def test_random_numbers_at_and_outside_their_ends(q, dev, v):
     p = np.zeros((6, 1, v), np.float32)
-    p[:, 0, [17, 4096, 4500, 8191, 8192, 8990]] = 0.125
+    p[:, 0, [17, 4096, 4500, 8191, 8192, v - 10]] = 0.125
     u = np.array([0.0, 1.0, 1.5, -1.0, np.nan, 1 - 2.0 ** -24], np.float32)[:, None]
     acc, out = call(q, dev, torch.from_numpy(p), None, np.zeros((6, 0), np.int32), None, u)
-    assert out[:, 0].tolist() == [17, 8990, 8990, 17, 8990, 8990]
+    assert out[:, 0].tolist() == [17, v - 10, v - 10, 17, v - 10, v - 10]
     one = torch.zeros((3, 1, v))
     one[0, 0, 0], one[1, 0, v - 1], one[2, 0, 4095] = 1.0, 1e-38, 3e38
     for x in (0.0, 0.5, 0.99999994):
@@ -135,10 +138,12 @@ def test_tests_of_drafts_are_exact(q, dev):
     assert np.array_equal(out[stands], np.tile([1, 2], (stands.sum(), 1)))
 
 
-def test_nothing_left_and_values_that_are_not_finite(q, dev):
-    v = 5000
+@pytest.mark.parametrize("more", [0, 40000])
+def test_nothing_left_and_values_that_are_not_finite(q, dev, more):
+    v = 5000 + more                                            # zeros behind the 5000
     nan, inf = float("nan"), float("inf")
     p = torch.full((7, 2, v), 1.0 / 8192)
+    p[:, :, 5000:] = 0
     qq = p[:, :1].clone()
     tokens = np.full((7, 1), 3, np.int32)
     u = np.tile(np.float32([1.0, 0.5]), (7, 1))                # 1 * q < p fails where they are equal
@@ -166,9 +171,9 @@ def test_drafts_outside_the_vocabulary(q, dev):
         assert got[0].tolist() == [0, 1, 2, 0, 3]
 
 
-def test_a_likeliest_draft_is_zeroed_wherever_it_stands(q, dev):
-    v = 8200
-    for d in (0, 1, 4095, 4096, 8191, 8199):
+@pytest.mark.parametrize("v", [8200, 30000])
+def test_a_likeliest_draft_is_zeroed_wherever_it_stands(q, dev, v):
+    for d in (0, 1, 1023, 1024, 4095, 4096, 8191, v - 1):
         p = torch.zeros((1, 2, v))
         p[0, 0, d], p[0, 0, (d + 5) % v] = 0.5, 0.5
         got = call(q, dev, p, None, np.array([[d]], np.int32), None, np.float32([[0.9, 0.1]]))
@@ -209,9 +214,9 @@ def test_rows_past_4_gib(q, dev):
 
 
 def test_graph_and_streams(q, dev):
-    cs = [case(rng(6, i), 4, 3, 10007, "f32", ragged=True) for i in range(4)]
+    cs = [case(rng(6, i), 4, 3, 20011, "f32", ragged=True) for i in range(4)]
     bufs = [cs[0][0].to(dev), cs[0][1].to(dev), *(up(a, dev) for a in cs[0][2:])]
-    ws = torch.empty(q.qmv_verify_drafts_workspace(4, 10007), dtype=torch.uint8, device=dev)
+    ws = torch.empty(q.qmv_verify_drafts_workspace(4, 20011), dtype=torch.uint8, device=dev)
     s = torch.cuda.Stream()
 
     def step(**kw):
@@ -251,7 +256,9 @@ def test_refusals_of_the_binding(q, dev):
                 {"p": a["p"][0]}, {"p": a["p"][:, :0]}):
         with pytest.raises(ValueError):
             q.qmv_verify_drafts(**{**a, **bad})
+    wide = torch.zeros((2, 1, 20000), device=dev)
     with pytest.raises(q.QmvError):
-        q.qmv_verify_drafts(**a, ws=torch.empty(8, dtype=torch.uint8, device=dev))
+        q.qmv_verify_drafts(wide, torch.empty((2, 0), dtype=torch.int32, device=dev), a["u"][:, :1].contiguous(),
+                            ws=torch.empty(8, dtype=torch.uint8, device=dev))
     with pytest.raises(q.QmvError):
         q.qmv_verify_drafts(**a, accepted=a["lengths"])

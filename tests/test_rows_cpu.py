@@ -157,7 +157,7 @@ def test_lora_workspaces():
     assert {L.qmm_lora_workspace(r, 5120, 5120, 64, e) // r for r in (1, 2, 7, 16) for e in (1, 3, 1024)} == {8 * 256}
 
 
-def verify(p=X, qq=Z, ty=F32, tok=IDS, ln=LEN, u=U, acc=DW, out=Y, r=3, d=4, v=1000, ws=TMP, wn=1 << 30):
+def verify(p=X, qq=Z, ty=F32, tok=IDS, ln=LEN, u=U, acc=DW, out=Y, r=3, d=4, v=20000, ws=TMP, wn=1 << 30):
     return L.qmv_verify_drafts(V(p), V(qq), ty, V(tok), V(ln), V(u), V(acc), V(out), r, d, v, V(ws), wn, None)
 
 
@@ -170,12 +170,13 @@ def test_verify_refusals():
     for name, base, by in (("p", X, 8), ("qq", Z, 4), ("tok", IDS, 2), ("ln", LEN, 1), ("u", U, 2), ("acc", DW, 2), ("out", Y, 2),
                            ("ws", TMP, 128)):
         assert verify(**{name: base + by}) == ALIGN, name
-    need = L.qmv_verify_drafts_workspace(3, 1000)
+    need = L.qmv_verify_drafts_workspace(3, 20000)
     assert need > 0 and verify(ws=0) == WORKSPACE and verify(wn=need - 1) == WORKSPACE
     for at in (X, Z, IDS, LEN, U):
         assert verify(acc=at) == ALIAS and verify(out=at) == ALIAS and verify(ws=at) == ALIAS
     assert verify(acc=Y) == ALIAS
     assert verify(r=0, p=0, u=0, acc=0, out=0) == OK
+    assert L.qmv_verify_drafts_workspace(3, 16384) == 0 and L.qmv_verify_drafts_workspace(3, 16385) == 3 * 17 * 16
     assert L.qmv_verify_drafts_workspace(3, 0) == 0 and L.qmv_verify_drafts_workspace(-1, 10) == 0
     assert q.qmv_verify_drafts_workspace(3, (1 << 32) + 10) == 0
 
