@@ -720,17 +720,46 @@ def _new(shape, dtype, device, stream, zeros=False):
         return (torch.zeros if zeros else torch.empty)(shape, dtype=dtype, device=device)
 
 
-def _work_memory(ws, need, device, index, stream):
-    """Address and size of the workspace, made where a call needs one and has none."""
+def _work_memory(ws, size, sizes, device, index, stream):
+    """Address and size of the workspace, made where a call needs one and has none; the C entry checks one that is given."""
     if ws is None:
+        need = size(*sizes)
         if not need:
             return None, 0
-        ws = _new(need, _U8[0], device, stream)
-    return _take(ws, "ws", _U8, (ws.numel(),), index), ws.numel()
+        ws = _new((need,), _U8[0], device, stream)
+    have = ws.numel()
+    return _take(ws, "ws", _U8, (have,), index), have
 
 
-def _or_none(t, name, types, shape, index):
-    return None if t is None else _take(t, name, types, shape, index)
+_MAY_BE_NONE = {"weights", "z", "dw", "row_index", "scale", "ranks", "q", "lengths"}
+
+
+def _addresses(index, *wanted):
+    """As _take, of several (tensor, name, types, shape); None for those that may be left out and are."""
+    out = []
+    for t, name, types, shape in wanted:
+        try:
+            if t.dtype in types and t.shape == shape and t.is_contiguous() and t.get_device() == index:   # host: -1
+                out.append(t.data_ptr())
+                continue
+        except AttributeError:
+            if t is None and name in _MAY_BE_NONE:
+                out.append(None)
+                continue
+        _explain(t, name, types, shape, index)
+    return out
+
+
+def _sizes(t, name, types, dims):
+    """Shape of a tensor whose device and type are checked later."""
+    try:
+        shape = t.shape
+        if len(shape) == dims:
+            return shape
+    except AttributeError:
+        pass
+    _dev(t, name, tuple(types))
+    raise ValueError(f"{name} has {t.dim()} dimensions, expected {dims}")
 
 
 def qmm_rows_sort_workspace(tokens: int, top_k: int, n_experts: int) -> int:
@@ -758,10 +787,9 @@ def qmm_rows_sort(ids, n_experts: int, offsets=None, row_index=None, places=None
         row_index = _new((tokens * top_k,), _I32[0], ids.device, stream)
     if places is None:
         places = _new((tokens, top_k), _I32[0], ids.device, stream)
-    args = (_take(ids, "ids", _I32, (tokens, top_k), index), _take(offsets, "offsets", _I32, (n_experts + 1,), index),
-            _take(row_index, "row_index", _I32, (tokens * top_k,), index),
-            _take(places, "places", _I32, (tokens, top_k), index))
-    wp, wn = _work_memory(ws, lib.qmm_rows_sort_workspace(tokens, top_k, n_experts), ids.device, index, stream)
+    args = _addresses(index, (ids, "ids", _I32, (tokens, top_k)), (offsets, "offsets", _I32, (n_experts + 1,)),
+                      (row_index, "row_index", _I32, (tokens * top_k,)), (places, "places", _I32, (tokens, top_k)))
+    wp, wn = _work_memory(ws, lib.qmm_rows_sort_workspace, (tokens, top_k, n_experts), ids.device, index, stream)
     _run(lib.qmm_rows_sort, name, index, stream, *args, tokens, top_k, n_experts, wp, wn)
     return offsets, row_index, places
 
@@ -774,9 +802,9 @@ def qmm_rows_spread(x, places, rows=None, out=None, stream=None):
     """
     name = "qmm_rows_spread"
     index, (tokens, h) = _first(x, "x", _FLOATS, 2, name)
-    _, (_, top_k) = _first(places, "places", _I32, 2, name)
+    _, top_k = _sizes(places, "places", _I32, 2)
     if out is not None:
-        _, (have, _) = _first(out, "out", (x.dtype,), 2, name)
+        have, _ = _sizes(out, "out", (x.dtype,), 2)
         if rows is not None and rows != have:
             raise ValueError(f"out has {have} rows, expected {rows}")
         rows = have
@@ -785,9 +813,9 @@ def qmm_rows_spread(x, places, rows=None, out=None, stream=None):
     _in_c(name, top_k, h, rows)
     if out is None:
         out = _new((rows, h), x.dtype, x.device, stream, zeros=True)
-    _run(lib.qmm_rows_spread, name, index, stream, _take(x, "x", _FLOATS, (tokens, h), index), _FLOATS[x.dtype],
-         _take(places, "places", _I32, (tokens, top_k), index), _take(out, "out", (x.dtype,), (rows, h), index), tokens,
-         top_k, h, rows)
+    xp, pp, op = _addresses(index, (x, "x", _FLOATS, (tokens, h)), (places, "places", _I32, (tokens, top_k)),
+                            (out, "out", (x.dtype,), (rows, h)))
+    _run(lib.qmm_rows_spread, name, index, stream, xp, _FLOATS[x.dtype], pp, op, tokens, top_k, h, rows)
     return out
 
 
@@ -799,14 +827,14 @@ def qmm_rows_combine(z, places, weights=None, y=None, out_dtype=None, stream=Non
     """
     name = "qmm_rows_combine"
     index, (rows, h) = _first(z, "z", _FLOATS, 2, name)
-    _, (tokens, top_k) = _first(places, "places", _I32, 2, name)
-    _in_c(name, top_k, h)
+    tokens, top_k = _sizes(places, "places", _I32, 2)
+    _in_c(name, tokens, top_k, h)
     if y is None:
         y = _new((tokens, h), out_dtype or _F32[0], z.device, stream)
     y_type = _y_type(y, out_dtype)
-    _run(lib.qmm_rows_combine, name, index, stream, _take(z, "z", _FLOATS, (rows, h), index), _FLOATS[z.dtype],
-         _take(places, "places", _I32, (tokens, top_k), index), _or_none(weights, "weights", _F32, (tokens, top_k), index),
-         _take(y, "y", _FLOATS, (tokens, h), index), y_type, tokens, top_k, h, rows)
+    zp, pp, wp, yp = _addresses(index, (z, "z", _FLOATS, (rows, h)), (places, "places", _I32, (tokens, top_k)),
+                                (weights, "weights", _F32, (tokens, top_k)), (y, "y", _FLOATS, (tokens, h)))
+    _run(lib.qmm_rows_combine, name, index, stream, zp, _FLOATS[z.dtype], pp, wp, yp, y_type, tokens, top_k, h, rows)
     return y
 
 
@@ -819,11 +847,11 @@ def qmm_rows_combine_grad(dy, z, places, weights=None, rows=None, dz=None, dw=No
     """
     name = "qmm_rows_combine_grad"
     index, (tokens, h) = _first(dy, "dy", _FLOATS, 2, name)
-    _, (_, top_k) = _first(places, "places", _I32, 2, name)
+    _, top_k = _sizes(places, "places", _I32, 2)
     same = (dy.dtype,)
     for t, what in ((dz, "dz"), (z, "z")):
         if t is not None:
-            _, (have, _) = _first(t, what, same, 2, name)
+            have, _ = _sizes(t, what, same, 2)
             if rows is not None and rows != have:
                 raise ValueError(f"{what} has {have} rows, expected {rows}")
             rows = have
@@ -836,10 +864,10 @@ def qmm_rows_combine_grad(dy, z, places, weights=None, rows=None, dz=None, dw=No
         dz = _new((rows, h), dy.dtype, dy.device, stream, zeros=True)
     if dw is None and z is not None:
         dw = _new((tokens, top_k), _F32[0], dy.device, stream)
-    _run(lib.qmm_rows_combine_grad, name, index, stream, _take(dy, "dy", _FLOATS, (tokens, h), index),
-         _or_none(z, "z", same, (rows, h), index), _FLOATS[dy.dtype], _take(places, "places", _I32, (tokens, top_k), index),
-         _or_none(weights, "weights", _F32, (tokens, top_k), index), _take(dz, "dz", same, (rows, h), index),
-         _or_none(dw, "dw", _F32, (tokens, top_k), index), tokens, top_k, h, rows)
+    yp, zp, pp, wp, dzp, dwp = _addresses(
+        index, (dy, "dy", _FLOATS, (tokens, h)), (z, "z", same, (rows, h)), (places, "places", _I32, (tokens, top_k)),
+        (weights, "weights", _F32, (tokens, top_k)), (dz, "dz", same, (rows, h)), (dw, "dw", _F32, (tokens, top_k)))
+    _run(lib.qmm_rows_combine_grad, name, index, stream, yp, zp, _FLOATS[dy.dtype], pp, wp, dzp, dwp, tokens, top_k, h, rows)
     return dz, dw
 
 
@@ -861,24 +889,21 @@ def qmm_lora(x, a, b, offsets, y, row_index=None, scale=None, ranks=None, base=N
     """
     name = "qmm_lora"
     index, (x_rows, k) = _first(x, "x", _BF16, 2, name)
-    _, (e, rank, _) = _first(a, "a", _BF16, 3, name)
-    _, (_, n, _) = _first(b, "b", _BF16, 3, name)
-    rows, found = x_rows, None
-    if row_index is not None:
-        rows = row_index.numel()
-        _rows_in_range(rows, name)
-        found = _take(row_index, "row_index", _I32, (rows,), index)
-    _in_c(name, rank, k, n)
-    _first(y, "y", _FLOATS, 2, name)
+    e, rank, _ = _sizes(a, "a", _BF16, 3)
+    _, n, _ = _sizes(b, "b", _BF16, 3)
+    _sizes(y, "y", _FLOATS, 2)
+    rows = x_rows if row_index is None else row_index.numel()
+    _in_c(name, rows, e, rank, k, n)
     y_type = _y_type(y, None)
-    yp = _take(y, "y", _FLOATS, (x_rows, n), index)
-    args = (_take(a, "a", _BF16, (e, rank, k), index), 2 * e * rank * k, _take(b, "b", _BF16, (e, n, rank), index),
-            2 * e * n * rank, _or_none(scale, "scale", _F32, (e,), index), _or_none(ranks, "ranks", _I32, (e,), index),
-            _take(x, "x", _BF16, (x_rows, k), index), _take(offsets, "offsets", _I32, (e + 1,), index), found,
-            yp if base is None else _take(base, "base", (y.dtype,), (x_rows, n), index), yp)
-    wp, wn = _work_memory(ws, lib.qmm_lora_workspace(rows, n, k, rank, e), x.device, index, stream)
+    ap, bp, sp, rp, xp, op, ip, yp = _addresses(
+        index, (a, "a", _BF16, (e, rank, k)), (b, "b", _BF16, (e, n, rank)), (scale, "scale", _F32, (e,)),
+        (ranks, "ranks", _I32, (e,)), (x, "x", _BF16, (x_rows, k)), (offsets, "offsets", _I32, (e + 1,)),
+        (row_index, "row_index", _I32, (rows,)), (y, "y", _FLOATS, (x_rows, n)))
+    from_ = yp if base is None else _take(base, "base", (y.dtype,), (x_rows, n), index)
+    wp, wn = _work_memory(ws, lib.qmm_lora_workspace, (rows, n, k, rank, e), x.device, index, stream)
     if rows:   # an empty row_index has no address, which would stand for rows in order
-        _run(lib.qmm_lora, name, index, stream, *args, y_type, rows, x_rows, n, k, rank, e, wp, wn)
+        _run(lib.qmm_lora, name, index, stream, ap, 2 * e * rank * k, bp, 2 * e * n * rank, sp, rp, xp, op, ip, from_, yp,
+             y_type, rows, x_rows, n, k, rank, e, wp, wn)
     return y
 
 
@@ -908,11 +933,10 @@ def qmv_verify_drafts(p, drafts, u, q=None, lengths=None, accepted=None, tokens=
         accepted = _new((requests,), _I32[0], p.device, stream)
     if tokens is None:
         tokens = _new((requests, steps), _I32[0], p.device, stream)
-    args = (_take(p, "p", _FLOATS, (requests, steps, vocab), index),
-            _or_none(q, "q", (p.dtype,), (requests, n, vocab), index), _FLOATS[p.dtype],
-            _take(drafts, "drafts", _I32, (requests, n), index), _or_none(lengths, "lengths", _I32, (requests,), index),
-            _take(u, "u", _F32, (requests, steps), index), _take(accepted, "accepted", _I32, (requests,), index),
-            _take(tokens, "tokens", _I32, (requests, steps), index))
-    wp, wn = _work_memory(ws, lib.qmv_verify_drafts_workspace(requests, vocab), p.device, index, stream)
-    _run(lib.qmv_verify_drafts, name, index, stream, *args, requests, n, vocab, wp, wn)
+    pp, qp, dp, lp, up, ap, tp = _addresses(
+        index, (p, "p", _FLOATS, (requests, steps, vocab)), (q, "q", (p.dtype,), (requests, n, vocab)),
+        (drafts, "drafts", _I32, (requests, n)), (lengths, "lengths", _I32, (requests,)), (u, "u", _F32, (requests, steps)),
+        (accepted, "accepted", _I32, (requests,)), (tokens, "tokens", _I32, (requests, steps)))
+    wp, wn = _work_memory(ws, lib.qmv_verify_drafts_workspace, (requests, vocab), p.device, index, stream)
+    _run(lib.qmv_verify_drafts, name, index, stream, pp, qp, _FLOATS[p.dtype], dp, lp, up, ap, tp, requests, n, vocab, wp, wn)
     return accepted, tokens

@@ -193,6 +193,83 @@ def test_binding_refuses_what_is_not_on_a_gpu():
         q.qmm_rows_sort([[1]], 4)
 
 
+class Fake:
+    """A contiguous device tensor by its attributes alone."""
+
+    def __init__(self, shape, dtype=torch.int32, address=1 << 20):
+        self.shape, self.dtype, self.device, self.address = torch.Size(shape), dtype, 0, address
+
+    def get_device(self):
+        return 0
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return self.address
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+
+HUGE = (1 << 32) + 5   # a C int of this value is 5
+
+
+def test_sizes_that_a_c_int_does_not_hold_are_refused(monkeypatch):
+    calls = []
+    monkeypatch.setattr(q, "_run", lambda *a: calls.append(a))
+    f, bf = torch.float32, torch.bfloat16
+    plan = (Fake((5,)), Fake((12,)), Fake((4, 3)))
+
+    def refused(call):
+        with pytest.raises(q.QmvError) as e:
+            call()
+        assert e.value.code == RANGE and calls == []
+
+    for t, k, e in ((HUGE, 3, 4), (4, HUGE, 4), (4, 3, HUGE)):
+        refused(lambda: q.qmm_rows_sort(Fake((t, k)), e, *plan))
+    for t, k, h, r in ((HUGE, 3, 8, 9), (4, HUGE, 8, 9), (4, 3, HUGE, 9), (4, 3, 8, HUGE)):
+        x, z, pl, w = Fake((t, h), f), Fake((r, h), f), Fake((t, k)), Fake((t, k), f)
+        refused(lambda: q.qmm_rows_spread(x, pl, out=z))
+        refused(lambda: q.qmm_rows_combine(z, pl, w, y=x))
+        refused(lambda: q.qmm_rows_combine_grad(x, z, pl, w, dz=z, dw=w))
+    for x_rows, rows, n, k, rank, e in ((HUGE, 7, 8, 8, 8, 1), (9, HUGE, 8, 8, 8, 1), (9, 7, HUGE, 8, 8, 1), (9, 7, 8, HUGE, 8, 1),
+                                        (9, 7, 8, 8, HUGE, 1), (9, 7, 8, 8, 8, HUGE)):
+        refused(lambda: q.qmm_lora(Fake((x_rows, k), bf), Fake((e, rank, k), bf), Fake((e, n, rank), bf), Fake((e + 1,)),
+                                   Fake((x_rows, n), f), row_index=Fake((rows,)), ws=Fake((1 << 20,), torch.uint8)))
+    for r, d, v in ((HUGE, 3, 100), (2, HUGE, 100), (2, 3, HUGE)):
+        refused(lambda: q.qmv_verify_drafts(Fake((r, d + 1, v), f), Fake((r, d)), Fake((r, d + 1), f), accepted=Fake((r,)),
+                                            tokens=Fake((r, d + 1))))
+    assert q.qmm_lora_workspace(HUGE, 64, 64, 16, 1) == 0 and q.qmm_lora_workspace(4, 64, HUGE + 3, 16, 1) == 0
+
+
+def test_what_may_be_left_out(monkeypatch):
+    calls = []
+    monkeypatch.setattr(q, "_run", lambda fn, name, index, stream, *a: calls.append(a))
+    f, bf = torch.float32, torch.bfloat16
+    x, z, pl = Fake((4, 8), f, 16), Fake((9, 8), f, 32), Fake((4, 3), address=48)
+    q.qmm_rows_combine(z, pl, y=x)
+    assert calls.pop()[3] is None
+    q.qmm_rows_combine_grad(x, None, pl, dz=z)
+    assert calls[-1][1] is None and calls[-1][4] is None and calls.pop()[6] is None
+    ws = Fake((1 << 20,), torch.uint8, 64)
+    a, b, off, y = Fake((2, 8, 16), bf), Fake((2, 10, 8), bf), Fake((3,)), Fake((4, 10), f, 80)
+    q.qmm_lora(Fake((4, 16), bf), a, b, off, y, ws=ws)
+    got = calls.pop()
+    assert got[4] is None and got[5] is None and got[8] is None and got[9] == got[10] == 80 and got[-2:] == (64, 1 << 20)
+    q.qmm_lora(Fake((4, 16), bf), a, b, off, y, row_index=Fake((0,), address=0), ws=ws)   # no rows: nothing is launched
+    assert calls == []
+    q.qmv_verify_drafts(Fake((2, 4, 100), f), Fake((2, 3)), Fake((2, 4), f), accepted=Fake((2,)), tokens=Fake((2, 4)))
+    got = calls.pop()
+    assert got[1] is None and got[4] is None and got[8:] == (2, 3, 100, None, 0)
+    for missing in ("z", "places"):
+        with pytest.raises(TypeError):
+            q.qmm_rows_combine(**{**dict(z=z, places=pl, y=x), missing: None})
+
+
 # ------------------------------------------------------------------ the oracle
 
 def test_sort_by_hand():
