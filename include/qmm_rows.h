@@ -59,8 +59,8 @@ int qmm_rows_sort(const int32_t *ids, int32_t *offsets, int32_t *row_index, int3
  *   out     [rows][h] of the same type, 16-byte aligned; rows that no place names
  *           are left as they were
  *   tokens >= 0, rows >= 0 (0: nothing is done), 1 <= h <= QMM_MAX_K
- * A row that several places name holds one of their tokens' values, which is
- * not defined. The gradient by x is qmm_rows_combine on out's, without weights.
+ * A row that several places name gets values of any of their tokens, in no
+ * defined mix. The gradient by x is qmm_rows_combine on out's, without weights.
  */
 int qmm_rows_spread(const void *x, int type, const int32_t *places, void *out, int tokens, int top_k, int h, int rows,
                     void *stream);
@@ -83,8 +83,7 @@ int qmm_rows_combine(const void *z, int z_type, const int32_t *places, const flo
  *   dz[places[t][j]] = w[t][j] * dy[t], in fp32, rounded once
  *   dw[t][j]         = sum_h dy[t] * z[places[t][j]], fp32 sums; 0 where a choice has no place
  *   dy, z, dz  of one `type`, 16-byte aligned; rows of dz that no place names
- *              are left as they were. A row that several places name is not
- *              defined in dz.
+ *              are left as they were; one that several name is not defined
  *   w          as above (NULL: weights of one)
  *   dw         fp32 [tokens][top_k], 4-byte aligned
  *   z and dw may both be NULL: dz alone

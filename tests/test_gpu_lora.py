@@ -99,7 +99,7 @@ class Case:
     (1, 1, 8, 8, 1), (1, 5120, 512, 16, 8), (2, 64, 64, 16, 2), (5, 65, 72, 8, 3), (16, 257, 200, 24, 5), (17, 300, 136, 32, 4),
     (40, 129, 1000, 40, 40), (64, 1000, 512, 64, 24), (63, 260, 264, 128, 3), (130, 190, 520, 72, 2), (300, 333, 200, 16, 3),
     (700, 259, 136, 64, 2), (400, 1100, 72, 104, 1), (100, 70, 64, 8, 1024), (530, 130, 72, 128, 1), (1100, 75, 64, 8, 2),
-    (1030, 66, 80, 24, 5)])
+    (1030, 66, 80, 24, 5), (1500, 40, 64, 8, 700)])
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 def test_against_the_oracle(q, dev, rows, n, k, rank, adapters, out):
     for mixed in (True, False):

@@ -126,6 +126,12 @@ def test_sort_of_many_choices_and_extreme_ids(q, dev):
         assert np.array_equal(got, exact)
 
 
+def test_sort_of_more_than_a_tile_a_part(q, dev):
+    ids = choices(rng(11), 1500001, 1, 77)
+    for got, exact in zip(sort_into_guards(q, dev, ids, 77), np_sort(ids, 77)):
+        assert np.array_equal(got, exact)
+
+
 def test_sort_without_tokens_or_some_outputs(q, dev):
     off, idx, pl = q.qmm_rows_sort(torch.empty((0, 4), dtype=torch.int32, device=dev), 3)
     assert host(off).tolist() == [0, 0, 0, 0] and idx.shape == (0,) and pl.shape == (0, 4)
@@ -320,6 +326,20 @@ def test_rows_past_4_gib(q, dev):
     assert bool((z[-1] == 9).all()) and bool((z[-2] == 9).all()) and bool((z[4:-2] == 0).all())
     dz, dw = q.qmm_rows_combine_grad(torch.ones((2, h), device=dev), z, places[:, :1].contiguous(), dz=z.clone())
     assert host(dw).tolist() == [[9 * h], [9 * h]] and bool((dz[-1] == 1).all()) and bool((dz[4:-2] == 0).all())
+
+
+def test_more_tokens_than_workgroups(q, dev):
+    # 2^20 + 3 tokens of 256 pieces each: the kernels take several tokens a workgroup
+    tokens, h = (1 << 20) + 3, 1024
+    z = torch.arange(tokens, device=dev, dtype=torch.float32)[:, None] + torch.arange(h, device=dev) / 2048
+    places = torch.arange(tokens - 1, -1, -1, device=dev, dtype=torch.int32)[:, None]
+    y = q.qmm_rows_combine(z, places)
+    assert torch.equal(y, z.flip(0))
+    assert torch.equal(q.qmm_rows_spread(y, places), z)
+    weights = torch.full((tokens, 1), 0.5, device=dev)
+    dz, dw = q.qmm_rows_combine_grad(torch.ones_like(z), z.flip(0).contiguous().sign_(), places, weights)
+    assert bool((dz == 0.5).all())
+    assert int((dw != h).sum()) == 1 and float(dw.min()) == h - 1            # ones, but for the first value of all
 
 
 # ------------------------------------------------------------------ calls as a program makes them

@@ -202,6 +202,16 @@ def test_nothing_to_do_and_more_requests(q, dev):
     assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
 
 
+def test_the_most_requests(q, dev):
+    c = case(rng(8), 65535, 1, 3, "f32")
+    got, want = call(q, dev, *c), wanted(*c)
+    assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+    p = torch.zeros((65535, 1, 16385))
+    p[:, 0, 16384] = 1
+    _, out = call(q, dev, p, None, np.zeros((65535, 0), np.int32), None, np.full((65535, 1), 0.3, np.float32))
+    assert (out == 16384).all()
+
+
 def test_rows_past_4_gib(q, dev):
     # p of 2^32 + values: the last request's rows lie behind 16 GiB
     r, v = 1030, 1 << 22
