@@ -52,10 +52,10 @@ inline bool past_caches(int rows, int width, bool f32) {
 
 constexpr int kKBlock = 64;   // values of k a wave takes at a time
 
-// Rows of one tile (one adapter's), the parts of k of the first product, the
-// columns of y of one workgroup of the second, and whether y goes past the caches.
-// The sums of a row go by the parts alone, and up to QMM_SAME_ROWS rows these go by
-// k alone.
+// Rows of one tile (one adapter's), the parts of k of the first product (0: both
+// products in one launch), the columns of y of one workgroup of the second, and
+// whether y goes past the caches. The sums of a row go by the parts alone, and up
+// to QMM_SAME_ROWS rows these go by n, k and rank.
 struct LoraPlan {
   int tile, splits, columns;
   bool far;
@@ -67,6 +67,17 @@ inline int lora_tiles(int rows, int n_adapters, int tile) {
 
 inline LoraPlan lora_plan(int rows, int n, int k, int rank, int n_adapters, int x_rows, bool y_f32) {
   LoraPlan p{};
+  // One launch, in which every workgroup of a tile takes all of A x, where a tile's
+  // x and A are few bytes for one CU, which gets some 60 GB/s of them, and all
+  // workgroups run at once: rank 16, one row of 2048 8.2 us against 9.2 by two, 64
+  // rows of 5 adapters 9.0 against 9.9; of 17408 columns 33 against 18. One row of
+  // 5120 takes 10.1 against 9.4 in a graph, but 10.1 against 12.6 launched from the
+  // host, which more rows do not (64 of 5 adapters 12.7 against 10.2 in a graph).
+  p.tile = 16;
+  p.columns = 1024;
+  const int few = lora_tiles(rows, n_adapters, 16) < 17 ? 17 : lora_tiles(rows, n_adapters, 16);
+  const int64_t most = rows <= QMM_SAME_ROWS ? 320 << 10 : 192 << 10;
+  if (rank <= 32 && (16 + rank) * (int64_t)k * 2 <= most && few * (int64_t)ceil_div(n, p.columns) <= 320) return p;
   // Long runs take tiles of 32 rows, which read A and B half as often: 8192 rows
   // of 5 adapters of 5120 x 5120, rank 64: 67 us against 90; 205 rows of each 22
   // against 24.4, 51 of each 19 against 16.4. Above rank 64 such a tile leaves one

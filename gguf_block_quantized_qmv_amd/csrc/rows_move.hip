@@ -4,7 +4,13 @@
 // All three are bound by memory: a row is read or written in pieces of 16 bytes,
 // one a lane, every byte once. Rows of any length and start are taken by the
 // same 16-byte instructions (the machine allows them at any address of the
-// element's own alignment), the last piece of a row by elements.
+// element's own alignment), the last piece of a row by elements. A thread keeps one
+// piece of a token for all its choices, so x is read once for top_k rows written,
+// and what a sum or a gradient needs of a token stays in registers.
+//
+// Rows of 2048 bf16, top 8: 8192 tokens spread 53 us (302 MB, 5.7 TB/s) and summed
+// back 51.5 us (302 MB, 5.9 TB/s), the gradient of 4096 tokens 55.5 us (285 MB, 5.1
+// TB/s); a large copy reaches 5.2 TB/s, a fill 6.8. Four tokens: 3 us, a launch.
 #include "qmv_device.h"
 #include "rows_internal.h"
 #include "rows_layout.h"
@@ -131,7 +137,8 @@ __global__ __launch_bounds__(256) void rows_spread_kernel(const MoveArgs p, cons
   }
 }
 
-// The rows of G choices are sent for together.
+// The rows of G choices are sent for together: with room for 8 of which top 2 has
+// two, six loads of eight are of row 0, so G is 2, 4 or 8 by top_k.
 template <bool ZF32, bool YF32, int A, int G, bool FAR>
 __global__ __launch_bounds__(256) void rows_combine_kernel(const MoveArgs p, const int shift, const int pieces) {
   constexpr int V = kValues<ZF32>;
@@ -180,7 +187,9 @@ __global__ __launch_bounds__(256) void rows_combine_kernel(const MoveArgs p, con
 
 // LANES lanes a token (a wave, or the whole workgroup), which keep the dot
 // products of G choices in registers and add them up at the end, in an order that
-// goes by the width alone.
+// goes by the width alone. The whole workgroup where a row has more pieces than a
+// wave: 4096 tokens of 2048 bf16, top 8, 62 us against a wave's 74. Groups of G
+// choices by top_k as above: 16384 tokens of top 2 54 us, with groups of 8 73.
 template <bool F32, int A, int LANES, int G, bool FAR>
 __global__ __launch_bounds__(256) void rows_combine_grad_kernel(const MoveArgs p, const int pieces) {
   constexpr int V = kValues<F32>;

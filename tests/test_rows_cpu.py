@@ -114,7 +114,7 @@ def test_combine_grad_refusals():
 
 
 def lora(a=A, an=None, b=B, bn=None, sc=SC, rk=RK, x=X, off=OFF, idx=IDX, base=Z, y=Y, ty=F32, rows=40, x_rows=50, n=200,
-         k=256, rank=16, e=4, ws=TMP, wn=1 << 30):
+         k=256, rank=40, e=4, ws=TMP, wn=1 << 30):
     an = 2 * e * rank * k if an is None else an
     bn = 2 * e * rank * n if bn is None else bn
     return L.qmm_lora(V(a), an, V(b), bn, V(sc), V(rk), V(x), V(off), V(idx), V(base), V(y), ty, rows, x_rows, n, k, rank, e,
@@ -129,12 +129,12 @@ def test_lora_refusals():
         assert lora(**bad) == RANGE, bad
     for bad in ({"n": 0}, {"k": 0}, {"k": 12}, {"rank": 0}, {"rank": 12}, {"rank": -8}, {"idx": 0}):
         assert lora(**bad) == SHAPE, bad
-    assert lora(an=0) == SIZE and lora(bn=2 * 4 * 16 * 200 - 1) == SIZE and lora(an=2 * 4 * 16 * 256 + 2) == SIZE
+    assert lora(an=0) == SIZE and lora(bn=2 * 4 * 40 * 200 - 1) == SIZE and lora(an=2 * 4 * 40 * 256 + 2) == SIZE
     for name, base in (("a", A), ("b", B), ("x", X), ("base", Z), ("y", Y)):
         assert lora(**{name: base + 8}) == ALIGN, name
     assert lora(sc=SC + 2) == ALIGN and lora(rk=RK + 1) == ALIGN and lora(off=OFF + 2) == ALIGN
     assert lora(idx=IDX + 2) == ALIGN and lora(ws=TMP + 64) == ALIGN
-    need = L.qmm_lora_workspace(40, 200, 256, 16, 4)
+    need = L.qmm_lora_workspace(40, 200, 256, 40, 4)
     assert need > 0 and lora(ws=0) == WORKSPACE and lora(wn=need - 1) == WORKSPACE
     for at in (A, B, SC, RK, X, OFF, IDX, Z + 16, TMP):
         assert lora(y=at) == ALIAS, hex(at)
@@ -153,6 +153,7 @@ def test_lora_workspaces():
                 b = L.qmm_lora_workspace(rows, 5120, k, 64, e)
                 # at most 16 parts of k, none without a block of 64
                 assert b % (rows * 64 * 4) == 0 and 1 <= b // (rows * 64 * 4) <= max(1, min(16, -(-k // 64))), (rows, k, e)
+    assert L.qmm_lora_workspace(1, 5120, 2048, 16, 8) == 0     # a small A: one launch
     # few rows: the parts of k, and so a row's bits, go by k alone
     assert {L.qmm_lora_workspace(r, 5120, 5120, 64, e) // r for r in (1, 2, 7, 16) for e in (1, 3, 1024)} == {8 * 256}
 
