@@ -18,8 +18,8 @@
 // launches included; 64 rows of 24 adapters, rank 32, k 5120, 17408 columns: 5.1 and
 // 9.4 us, where a large copy would take 4.6 for the bytes). Long runs: the L2, of which a CU
 // gets some 24 bytes a cycle, since each tile of 32 rows reads all of A and B (4096
-// rows of 5 adapters, rank 64, 5120 x 5120, bf16: 16.8 and 24.3 us, 42 MB read and
-// 84 MB read and written, 2.5 and 3.4 TB/s of a large copy's 5.2; the products alone
+// rows of 5 adapters, rank 64, 5120 x 5120, bf16: 13.5 and 24.3 us, 42 MB read and
+// 84 MB read and written, 3.1 and 3.4 TB/s of a large copy's 5.2; the products alone
 // would be 2 and 7 us at a large library product's rate). Both products of 16 rows in
 // one workgroup read A and B twice as often and took 51 us; tiles of 64 rows gained
 // nothing over 32.

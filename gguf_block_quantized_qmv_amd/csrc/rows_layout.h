@@ -76,8 +76,8 @@ inline LoraPlan lora_plan(int rows, int n, int k, int rank, int n_adapters, int 
   p.tile = 16;
   p.columns = 1024;
   const int few = lora_tiles(rows, n_adapters, 16) < 17 ? 17 : lora_tiles(rows, n_adapters, 16);
-  const int64_t most = rows <= QMM_SAME_ROWS ? 320 << 10 : 192 << 10;
-  if (rank <= 32 && (16 + rank) * (int64_t)k * 2 <= most && few * (int64_t)ceil_div(n, p.columns) <= 320) return p;
+  const int64_t bytes = rows <= QMM_SAME_ROWS ? 320 << 10 : 192 << 10;
+  if (rank <= 32 && (16 + rank) * (int64_t)k * 2 <= bytes && few * (int64_t)ceil_div(n, p.columns) <= 320) return p;
   // Long runs take tiles of 32 rows, which read A and B half as often: 8192 rows
   // of 5 adapters of 5120 x 5120, rank 64: 67 us against 90; 205 rows of each 22
   // against 24.4, 51 of each 19 against 16.4. Above rank 64 such a tile leaves one
@@ -89,6 +89,13 @@ inline LoraPlan lora_plan(int rows, int n, int k, int rank, int n_adapters, int 
   // tiles fill the CUs (512 rows of rank 128: 4 parts 28.7, 8 33.7).
   p.splits = blocks / 10 < ceil_div(256, tiles) ? blocks / 10 : ceil_div(256, tiles);
   p.splits = p.splits < 1 ? 1 : p.splits > 16 ? 16 : p.splits;
+  // One more where that takes a fifth off the CU with the most: of 4096 rows of 5
+  // adapters, rank 64, some 130 tiles, 3 parts 40.0 us, 2 42.7, 1 46.2, 4 41.1; of 3000
+  // 4 parts 37.2, 3 39.4. An adapter's last tile is taken for half full.
+  const int some = rows / p.tile + (tiles - rows / p.tile) / 2, more = p.splits + 1;
+  const int64_t most_now = ceil_div((int64_t)some * p.splits, 256), most_then = ceil_div((int64_t)some * more, 256);
+  if (rows > QMM_SAME_ROWS && more <= 16 && more <= blocks / 10 && most_then * p.splits * 5 <= most_now * more * 4)
+    p.splits = more;
   // As many columns' shares as let all workgroups run at once, but for an eighth:
   // `waves` a SIMD is what the second kernel's registers allow. 64 rows of 24
   // adapters by 512 of 17408 columns 15.6 us, by 256 17.6; 4096 rows of rank 64 by
