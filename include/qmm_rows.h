@@ -113,8 +113,8 @@ size_t qmm_lora_workspace(int rows, int n, int k, int rank, int n_adapters);
  *              qmm_rows_sort (top_k = 1) gives them: row row_index[r] of x, base
  *              and y for r in offsets[e] .. offsets[e+1] - 1. An index outside
  *              [0, x_rows) is passed over. NULL: row r, and x_rows must equal
- *              rows. A row of x in two runs gets one of the two sums, which is
- *              not defined.
+ *              rows. A row of x that stands in the runs twice gets values of no
+ *              defined sum in y.
  *   base, y    [x_rows][n] of y_type (QMM_F32 or QMM_BF16), 16-byte aligned; the
  *              same array or two without a shared byte. Rows in no run are left
  *              as they were in y.
