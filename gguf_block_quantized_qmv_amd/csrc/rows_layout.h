@@ -68,16 +68,21 @@ inline int lora_tiles(int rows, int n_adapters, int tile) {
 inline LoraPlan lora_plan(int rows, int n, int k, int rank, int n_adapters, int x_rows, bool y_f32) {
   LoraPlan p{};
   // One launch, in which every workgroup of a tile takes all of A x, where a tile's
-  // x and A are few bytes for one CU, which gets some 60 GB/s of them, and all
-  // workgroups run at once: rank 16, one row of 2048 8.2 us against 9.2 by two, 64
-  // rows of 5 adapters 9.0 against 9.9; of 17408 columns 33 against 18. One row of
-  // 5120 takes 10.1 against 9.4 in a graph, but 10.1 against 12.6 launched from the
-  // host, which more rows do not (64 of 5 adapters 12.7 against 10.2 in a graph).
+  // x and A are few bytes for one CU, which gets some 60 GB/s of them, and workgroups
+  // have a CU each: rank 16, one row of 2048 8.2 us against 9.2 by two, 64 rows of 5
+  // adapters 9.0 against 9.9, 2000 of rank 32 13.9 against 15.7, 4200 by 1024 columns
+  // 19.9 against 16.8; 64 adapters of 5120 x 17408 33 against 18. One row of 5120 takes
+  // 10.1 against 9.4 in a graph, but 10.1 against 12.6 launched from the host, which
+  // more rows do not (64 of 5 adapters 12.7 against 10.2 in a graph). An adapter's
+  // last tile is taken for half full; up to QMM_SAME_ROWS rows the choice is that of
+  // as many tiles as they can have.
   p.tile = 16;
   p.columns = 1024;
-  const int few = lora_tiles(rows, n_adapters, 16) < 17 ? 17 : lora_tiles(rows, n_adapters, 16);
-  const int64_t bytes = rows <= QMM_SAME_ROWS ? 320 << 10 : 192 << 10;
-  if (rank <= 32 && (16 + rank) * (int64_t)k * 2 <= bytes && few * (int64_t)ceil_div(n, p.columns) <= 320) return p;
+  const bool few = rows <= QMM_SAME_ROWS;
+  const int all = few ? 17 : rows / 16 + (lora_tiles(rows, n_adapters, 16) - rows / 16) / 2;
+  if (rank <= 32 && (16 + rank) * (int64_t)k * 2 <= (few ? 320 << 10 : 192 << 10) &&
+      all * (int64_t)ceil_div(n, p.columns) <= (few ? 320 : 256))
+    return p;
   // Long runs take tiles of 32 rows, which read A and B half as often: 8192 rows
   // of 5 adapters of 5120 x 5120, rank 64: 67 us against 90; 205 rows of each 22
   // against 24.4, 51 of each 19 against 16.4. Above rank 64 such a tile leaves one

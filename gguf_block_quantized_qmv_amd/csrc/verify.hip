@@ -90,7 +90,7 @@ __device__ __forceinline__ int drafts_of(const VerifyArgs &a, int r) {
 }
 
 // Lane i of every wave holds draft i against its row.
-__device__ __forceinline__ Outcome judge(const VerifyArgs &a, int r) {
+__device__ __forceinline__ Outcome decide(const VerifyArgs &a, int r) {
   const int lane = (int)threadIdx.x & 63;
   const int length = drafts_of(a, r);
   bool stands = false;
@@ -257,7 +257,7 @@ template <bool F32>
 __global__ __launch_bounds__(256) void verify_sums_kernel(const VerifyArgs a, const int chunks) {
   const int r = (int)blockIdx.y, chunk = (int)blockIdx.x * 4 + ((int)threadIdx.x >> 6);
   if (chunk >= chunks) return;
-  const Outcome o = judge(a, r);
+  const Outcome o = decide(a, r);
   if (chunk == 0 && (threadIdx.x & 63) == 0) a.accepted[r] = o.accepted;
   sum_chunk<F32>(a, r, o, chunk, a.sums + (size_t)r * chunks * 2);
 }
@@ -278,7 +278,7 @@ __global__ __launch_bounds__(1024) void verify_whole_kernel(const VerifyArgs a, 
   extern __shared__ double sums[];
   const int r = (int)blockIdx.x, wave = (int)threadIdx.x >> 6;
   const float u = a.u[(size_t)r * (a.drafts + 1) + a.drafts];
-  const Outcome o = judge(a, r);
+  const Outcome o = decide(a, r);
   for (int c = wave; c < chunks; c += 16) sum_chunk<F32>(a, r, o, c, sums);
   __syncthreads();
   if (wave) return;

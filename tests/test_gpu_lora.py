@@ -114,6 +114,14 @@ def test_lengths_of_k(q, dev, k):
         c.holds(c.run(q, dev))
 
 
+@pytest.mark.parametrize("rank", [16, 40, 96])
+@pytest.mark.parametrize("rows,parts", [(1000, 4), (2049, 4), (3000, 4), (4200, 3)])
+def test_long_runs_in_several_parts_of_k(q, dev, rows, rank, parts):
+    assert rank != 40 or q.qmm_lora_workspace(rows, 70, 2600, rank, 5) == parts * rows * rank * 4
+    c = Case(rng(rows, rank), rows, 70, 2600, rank, 5, "bf16")
+    c.holds(c.run(q, dev))
+
+
 @pytest.mark.parametrize("rows", [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 200])
 @pytest.mark.parametrize("rank", [16, 40, 128])
 def test_one_adapter_for_all(q, dev, rows, rank):   # tiles of 16 rows, and of 32 from 128 (512) rows on

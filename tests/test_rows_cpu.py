@@ -154,6 +154,8 @@ def test_lora_workspaces():
                 # at most 16 parts of k, none without a block of 64
                 assert b % (rows * 64 * 4) == 0 and 1 <= b // (rows * 64 * 4) <= max(1, min(16, -(-k // 64))), (rows, k, e)
     assert L.qmm_lora_workspace(1, 5120, 2048, 16, 8) == 0     # a small A: one launch
+    # many: parts of k that fill the CUs evenly, 130 tiles by 3
+    assert L.qmm_lora_workspace(4096, 5120, 5120, 64, 5) == 3 * 4096 * 64 * 4
     # few rows: the parts of k, and so a row's bits, go by k alone
     assert {L.qmm_lora_workspace(r, 5120, 5120, 64, e) // r for r in (1, 2, 7, 16) for e in (1, 3, 1024)} == {8 * 256}
 
