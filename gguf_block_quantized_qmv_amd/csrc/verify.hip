@@ -198,7 +198,10 @@ __device__ __forceinline__ void pick(const VerifyArgs &a, int r, const Outcome &
   upto[0] = wave_upto(own[0]);
   upto[1] = wave_upto(own[1]);
   const int kind = of_lane(upto[0], 63) > 0.0 ? 0 : 1;   // without a weight: p's own
-  const double total = of_lane(kind ? upto[1] : upto[0], 63), target = (double)u * total;
+  const double total = of_lane(kind ? upto[1] : upto[0], 63);
+  // From one on (or NaN) no running sum may lie above it: these are of another order than the whole and can
+  // round above it before the last weight.
+  const double target = u < 1.0f ? (double)u * total : __builtin_inf();
   int token = -1;
   if (total > 0.0) {
     // the first chunk whose running sum lies above the target, else the last with a weight

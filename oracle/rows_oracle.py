@@ -112,7 +112,8 @@ def verify_one(p, q, drafts, u):
     total = math.fsum(weights)
     if total <= 0:
         return n, -1
-    target, run, last = float(u[-1]) * total, 0.0, -1
+    # from one on: the last weight, although a running sum may round above the whole
+    target, run, last = float(u[-1]) * total if u[-1] < 1 else math.inf, 0.0, -1
     for i, v in enumerate(weights):
         if v > 0:
             run += v

@@ -272,3 +272,28 @@ def test_refusals_of_the_binding(q, dev):
                             ws=torch.empty(8, dtype=torch.uint8, device=dev))
     with pytest.raises(q.QmvError):
         q.qmv_verify_drafts(**a, accepted=a["lengths"])
+
+
+@pytest.mark.parametrize("v", [8000, 32768])
+@pytest.mark.parametrize("left", ["all", "rest"])
+def test_a_random_number_of_one_picks_the_last_weight_of_any(q, dev, v, left):
+    # sums that round: the whole may lie below a running sum of another order, and weights at the end below half its last bit
+    g = rng(9, v)
+    n = 64
+    p = softmax(4 * g.standard_normal((n, 2, v)))
+    p[:, :, v - 9:] = 0
+    last = g.integers(v - 9, v, n)
+    p[np.arange(n), 0, last] = 1e-30
+    p = torch.from_numpy(p.astype(np.float32))
+    tokens, u = np.zeros((n, 1), np.int32), np.ones((n, 2), np.float32)
+    u[::3, 1] = np.float32([1 + 2.0 ** -23, np.inf, np.nan])[np.arange(len(u[::3])) % 3]
+    qq = None
+    if left == "rest":                                         # 1 * q < p does not hold, and half of p is left of every token
+        p[:, 0, 0] = 0
+        qq = p[:, :1] / 2
+    lengths = np.full(n, 0 if left == "all" else 1, np.int32)
+    c = (p, qq, tokens, lengths, u)
+    got, want = call(q, dev, *c), wanted(*c)
+    assert want[0].tolist() == got[0].tolist() == [0] * n
+    assert want[1][:, 0].tolist() == last.tolist()
+    assert got[1][:, 0].tolist() == last.tolist()

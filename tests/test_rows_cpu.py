@@ -3,6 +3,7 @@ include/qmv_verify.h declare, refuses every malformed call before any HIP call, 
 use is pinned by values worked out by hand."""
 
 import ctypes
+import math
 import os
 import re
 
@@ -334,3 +335,12 @@ def test_verify_by_hand():
     assert o.verify_one([[0.0, np.nan]], None, [], [0.5]) == (0, -1)
     acc, out = o.verify([p], [qq], [[0, 0]], [1], [[0.4, 0.9, 0.3]])       # 0.1 + 0.2 lies above 0.3 in 64 bits
     assert acc.tolist() == [1] and out.tolist() == [[0, 1, -1]]
+
+
+def test_verify_picks_the_last_weight_from_one_on():
+    # 0.8 + 0.9 + 0.7 added one by one lies above their sum rounded once
+    w = [0.8, 0.9, 0.7, 1e-30, 0.0]
+    assert w[0] + w[1] + w[2] > math.fsum(w)
+    for u in (1.0, 1 + 2.0 ** -23, 7.0, math.inf, math.nan):
+        assert o.verify_one([w], None, [], [u]) == (0, 3), u
+    assert o.verify_one([w], None, [], [1 - 2.0 ** -24]) == (0, 2)
