@@ -728,14 +728,16 @@ def _need(name, *sizes):
 
 
 def _work_memory(ws, name, sizes, device, index, stream):
-    """Address and size of the workspace, made where a call needs one and has none; the C entry checks one that is given."""
+    """Address and size of the workspace, and itself, made where a call needs one and has none; the C entry checks one that
+    is given. Its caller keeps it until the call has been made: memory let go of before could be given to another thread's
+    call on this stream in between."""
     if ws is None:
         need = _need(name, *sizes)
         if not need:
-            return None, 0
+            return None, 0, None
         ws = _new((need,), _U8[0], device, stream)
     have = ws.numel()
-    return _take(ws, "ws", _U8, (have,), index), have
+    return _take(ws, "ws", _U8, (have,), index), have, ws
 
 
 _MAY_BE_NONE = {"weights", "z", "dw", "row_index", "scale", "ranks", "q", "lengths"}
@@ -796,7 +798,7 @@ def qmm_rows_sort(ids, n_experts: int, offsets=None, row_index=None, places=None
         places = _new((tokens, top_k), _I32[0], ids.device, stream)
     args = _addresses(index, (ids, "ids", _I32, (tokens, top_k)), (offsets, "offsets", _I32, (n_experts + 1,)),
                       (row_index, "row_index", _I32, (tokens * top_k,)), (places, "places", _I32, (tokens, top_k)))
-    wp, wn = _work_memory(ws, "qmm_rows_sort_workspace", (tokens, top_k, n_experts), ids.device, index, stream)
+    wp, wn, ws = _work_memory(ws, "qmm_rows_sort_workspace", (tokens, top_k, n_experts), ids.device, index, stream)
     _run(lib.qmm_rows_sort, name, index, stream, *args, tokens, top_k, n_experts, wp, wn)
     return offsets, row_index, places
 
@@ -907,7 +909,7 @@ def qmm_lora(x, a, b, offsets, y, row_index=None, scale=None, ranks=None, base=N
         (ranks, "ranks", _I32, (e,)), (x, "x", _BF16, (x_rows, k)), (offsets, "offsets", _I32, (e + 1,)),
         (row_index, "row_index", _I32, (rows,)), (y, "y", _FLOATS, (x_rows, n)))
     from_ = yp if base is None else _take(base, "base", (y.dtype,), (x_rows, n), index)
-    wp, wn = _work_memory(ws, "qmm_lora_workspace", (rows, n, k, rank, e), x.device, index, stream)
+    wp, wn, ws = _work_memory(ws, "qmm_lora_workspace", (rows, n, k, rank, e), x.device, index, stream)
     if rows:   # an empty row_index has no address, which would stand for rows in order
         _run(lib.qmm_lora, name, index, stream, ap, 2 * e * rank * k, bp, 2 * e * n * rank, sp, rp, xp, op, ip, from_, yp,
              y_type, rows, x_rows, n, k, rank, e, wp, wn)
@@ -944,6 +946,6 @@ def qmv_verify_drafts(p, drafts, u, q=None, lengths=None, accepted=None, tokens=
         index, (p, "p", _FLOATS, (requests, steps, vocab)), (q, "q", (p.dtype,), (requests, n, vocab)),
         (drafts, "drafts", _I32, (requests, n)), (lengths, "lengths", _I32, (requests,)), (u, "u", _F32, (requests, steps)),
         (accepted, "accepted", _I32, (requests,)), (tokens, "tokens", _I32, (requests, steps)))
-    wp, wn = _work_memory(ws, "qmv_verify_drafts_workspace", (requests, vocab), p.device, index, stream)
+    wp, wn, ws = _work_memory(ws, "qmv_verify_drafts_workspace", (requests, vocab), p.device, index, stream)
     _run(lib.qmv_verify_drafts, name, index, stream, pp, qp, _FLOATS[p.dtype], dp, lp, up, ap, tp, requests, n, vocab, wp, wn)
     return accepted, tokens

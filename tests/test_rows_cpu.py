@@ -6,6 +6,7 @@ import ctypes
 import math
 import os
 import re
+import weakref
 
 import numpy as np
 import pytest
@@ -272,6 +273,27 @@ def test_what_may_be_left_out(monkeypatch):
     for missing in ("z", "places"):
         with pytest.raises(TypeError):
             q.qmm_rows_combine(**{**dict(z=z, places=pl, y=x), missing: None})
+
+
+def test_a_workspace_that_the_binding_makes_lives_until_the_call_has_been_made(monkeypatch):
+    # let go of before, another thread's call on the same stream could be given its memory in between
+    made, calls = [], []
+
+    def new(shape, dtype, *a, **kw):
+        t = Fake(shape, dtype)
+        if dtype == torch.uint8:
+            made.append(weakref.ref(t))
+        return t
+
+    monkeypatch.setattr(q, "_new", new)
+    monkeypatch.setattr(q, "_run", lambda fn, name, *a: calls.append((name, [m() is not None for m in made])))
+    f, bf = torch.float32, torch.bfloat16
+    q.qmm_rows_sort(Fake((5000, 8)), 128)
+    q.qmm_lora(Fake((40, 256), bf), Fake((4, 40, 256), bf), Fake((4, 200, 40), bf), Fake((5,)), Fake((40, 200), f))
+    q.qmv_verify_drafts(Fake((3, 5, 20000), f), Fake((3, 4)), Fake((3, 5), f))
+    assert [c[0] for c in calls] == ["qmm_rows_sort", "qmm_lora", "qmv_verify_drafts"]
+    assert [c[1][-1] for c in calls] == [True] * 3 and len(made) == 3
+    assert [m() for m in made] == [None] * 3                   # and no longer
 
 
 # ------------------------------------------------------------------ the oracle
