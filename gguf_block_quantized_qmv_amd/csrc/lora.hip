@@ -10,8 +10,9 @@
 // With a small A and no more workgroups than CUs both are one launch (lora_plan).
 //
 // h keeps its 24 bits through the matrix cores: cut into three bf16 values of
-// eight bits each, hi + mid + lo == h, three instructions for one. The products
-// are exact in fp32, so y loses what fp32 additions lose.
+// eight bits each, hi + mid + lo == h but for bits below 2^-133, the smallest bf16
+// value, three instructions for one. The products are exact in fp32, so y loses
+// what fp32 additions lose.
 //
 // What bounds it. Few rows: a launch and trips to memory one behind the other, the
 // run's offsets, its index, A and x, then B (one row, rank 16, 5120 x 5120: 10 us,
@@ -199,8 +200,8 @@ struct Down {
   }
 };
 
-// v as three bf16 values of eight significant bits each that add up to it exactly.
-// What is not finite goes whole into the first.
+// v as three bf16 values of eight significant bits each that add up to it exactly,
+// but for bits below 2^-133. What is not finite goes whole into the first.
 __device__ __forceinline__ void cut_in_three(float v, uint32_t (&out)[3]) {
   const bool finite = (__builtin_bit_cast(uint32_t, v) & 0x7F800000u) != 0x7F800000u;
   const __bf16 whole = (__bf16)v;

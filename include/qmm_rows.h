@@ -100,8 +100,9 @@ size_t qmm_lora_workspace(int rows, int n, int k, int rank, int n_adapters);
 /*
  * Low-rank adapters of many requests beside a shared projection:
  *   y[r] = base[r] + scale[e] * B_e (A_e x[r])
- * for the rows r of adapter e's run, with fp32 sums (A_e x[r] included), rounded
- * once to y's type. With base == y the projection's result is added to in place.
+ * for the rows r of adapter e's run, with fp32 sums (A_e x[r] included; bits of
+ * scale[e] * (A_e x[r]) below 2^-133 are cut), rounded once to y's type. With
+ * base == y the projection's result is added to in place.
  *   a          bf16 [n_adapters][rank][k], 16-byte aligned, a_bytes == 2*n_adapters*rank*k
  *   b          bf16 [n_adapters][n][rank], 16-byte aligned, b_bytes == 2*n_adapters*n*rank
  *   scale      fp32 [n_adapters] or NULL (ones)

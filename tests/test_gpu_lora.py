@@ -364,3 +364,21 @@ def test_refusals_of_the_binding(q, dev):
     with pytest.raises(q.QmvError):                            # y in part over its own base
         both = torch.zeros((8, 40), device=dev)
         call(y=both[:6], base=both[2:])
+
+
+@pytest.mark.parametrize("rank", [16, 40])                     # one launch, and two
+def test_small_values_keep_their_bits_down_to_the_smallest_bf16_value(q, dev, rank):
+    # scale times A x of 24 bits down to below bf16's smallest value: every bit from 2^-133 on comes out, none below
+    g = rng(14)
+    n = 64
+    scale = (g.integers(1 << 23, 1 << 24, n) * 2.0 ** g.integers(-70, -20, n)).astype(np.float32)
+    x = torch.full((n, 8), 2.0 ** -40, dtype=torch.bfloat16)
+    a, b = torch.zeros((n, rank, 8), dtype=torch.bfloat16), torch.zeros((n, 9, rank), dtype=torch.bfloat16)
+    a[:, 3, 5], b[:, :, 3] = 2.0 ** -50, 2.0 ** 110
+    y = torch.zeros((n, 9), device=dev)
+    q.qmm_lora(x.to(dev), a.to(dev), b.to(dev), torch.arange(n + 1, dtype=torch.int32, device=dev), y, scale=up(scale, dev))
+    h = scale.astype(np.float64) * 2.0 ** -90
+    h = np.where(h < 2.0 ** -126, h.astype(np.float32).astype(np.float64), h)   # fp32's own smallest values
+    cut = np.floor(h * 2.0 ** 133) * 2.0 ** -133
+    assert 5 < (cut != h).sum() < 40 and (cut == 0).any() and (cut > 2.0 ** -105).any()
+    assert np.array_equal(f64(y), np.tile(cut[:, None] * 2.0 ** 110, (1, 9)))
