@@ -11,6 +11,7 @@ zeros, which add nothing). The sum with base rounds once: 2^-24 of the value. A 
 import numpy as np
 import pytest
 
+import lora_cases as cases
 from gpu_util import device, guarded, guards_intact, host
 from oracle import rows_oracle as o
 
@@ -382,3 +383,32 @@ def test_small_values_keep_their_bits_down_to_the_smallest_bf16_value(q, dev, ra
     cut = np.floor(h * 2.0 ** 133) * 2.0 ** -133
     assert 5 < (cut != h).sum() < 40 and (cut == 0).any() and (cut > 2.0 ** -105).any()
     assert np.array_equal(f64(y), np.tile(cut[:, None] * 2.0 ** 110, (1, 9)))
+
+
+@pytest.mark.parametrize("k", cases.KS)
+@pytest.mark.parametrize("rows,rank", cases.ROWS_RANKS)
+def test_whole_numbers(q, dev, rows, rank, k):
+    # no tolerance: a block of k that is lost, taken twice or from elsewhere changes some result
+    for n, out in ((67, "f32"), (1, "f32"), (130, "bf16")):
+        c = cases.whole_numbers(rows, n, k, rank)
+        want = torch.from_numpy(cases.result(c)).float().to(TYPES[out])
+        assert n == 1 or bool((want != torch.from_numpy(c["base"])).any())
+        y, buf = guarded((rows, n), TYPES[out], dev)
+        y.copy_(torch.from_numpy(c["base"]))
+        x, a, b = (torch.from_numpy(c[v]).to(dev).bfloat16() for v in "xab")
+        q.qmm_lora(x, a, b, up(c["offsets"], dev), y, row_index=up(c["index"], dev), scale=up(c["scale"], dev),
+                   ranks=up(c["ranks"], dev))
+        torch.cuda.synchronize()
+        assert guards_intact(buf)
+        assert torch.equal(y.cpu(), want)
+
+
+@pytest.mark.parametrize("k", [8, 64, 2600])
+@pytest.mark.parametrize("rank", [8, 16, 40, 128])
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+def test_one_row_and_one_column(q, dev, k, rank, out):
+    for rows, n in ((1, 1), (1, 64), (3, 1), (3, 2)):
+        c = Case(rng(k, rank, rows), rows, n, k, rank, 2, out, owner=np.zeros(rows), mixed=False)
+        c.base.mul_(2.0 ** -20)                                # the adapter's part is what counts
+        assert c.exact()[1].min() > 0
+        c.holds(c.run(q, dev))

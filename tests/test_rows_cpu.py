@@ -13,6 +13,7 @@ import pytest
 import torch
 
 import gguf_block_quantized_qmv_amd as q
+import lora_cases as cases
 from oracle import rows_oracle as o
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -366,3 +367,26 @@ def test_verify_picks_the_last_weight_from_one_on():
     for u in (1.0, 1 + 2.0 ** -23, 7.0, math.inf, math.nan):
         assert o.verify_one([w], None, [], [u]) == (0, 3), u
     assert o.verify_one([w], None, [], [1 - 2.0 ** -24]) == (0, 2)
+
+
+@pytest.mark.parametrize("rows,rank", cases.ROWS_RANKS)
+def test_every_block_of_k_counts_in_the_whole_numbers(rows, rank):
+    # a block of 64 lost, taken twice, or a row's blocks taken from their neighbour's places: some result differs
+    for k in cases.KS:
+        c = cases.whole_numbers(rows, 67, k, rank)
+        y, adds = cases.result(c), cases.by_block(c, 0)
+        assert np.array_equal(adds.sum(0) + c["base"][0], y[0]) and len(adds) == -(-k // 64)
+        assert adds.any(axis=1).all(), k
+        assert np.abs(y).max() < 1 << 24
+        if k > 64:
+            assert (cases.result(c, np.roll(c["a"], 64, axis=2))[0] != y[0]).any()
+        e, rows_of = c["owner"], np.abs(c["x"]).sum(1).max()
+        assert 2 * rows_of * rank + 8 < 1 << 24 and (e == 0).any()
+
+
+def test_whole_numbers_take_both_plans():
+    one = {(rows, k, rank): q.qmm_lora_workspace(rows, 67, k, rank, cases.ADAPTERS) == 0 for rows, rank in cases.ROWS_RANKS
+           for k in cases.KS}
+    assert set(one.values()) == {True, False}
+    for rows in (1, 16, 40, 300):                              # the change from one to two launches lies within
+        assert {v for (r, _, rank), v in one.items() if r == rows and rank <= 32} == {True, False}, rows
