@@ -7,7 +7,7 @@
 // operand of v_mfma_f32_16x16x32_bf16 and x as its B operand, cuts k into parts
 // for workgroups and those into blocks of 64 for their four waves, and leaves
 // fp32 sums by part. The second adds the parts, scales them and multiplies by B.
-// With a small A and no more workgroups than CUs both are one launch (lora_plan).
+// With a small A and workgroups that should have a CU each both are one launch (lora_plan).
 //
 // h keeps its 24 bits through the matrix cores: cut into three bf16 values of
 // eight bits each, hi + mid + lo == h but for bits below 2^-133, the smallest bf16

@@ -51,6 +51,7 @@ inline bool past_caches(int rows, int width, bool f32) {
 // ---- adapters --------------------------------------------------------------------
 
 constexpr int kKBlock = 64;   // values of k a wave takes at a time
+constexpr int kCus = 256;     // compute units
 
 // Rows of one tile (one adapter's), the parts of k of the first product (0: both
 // products in one launch), the columns of y of one workgroup of the second, and
@@ -67,21 +68,30 @@ inline int lora_tiles(int rows, int n_adapters, int tile) {
 
 inline LoraPlan lora_plan(int rows, int n, int k, int rank, int n_adapters, int x_rows, bool y_f32) {
   LoraPlan p{};
-  // One launch, in which every workgroup of a tile takes all of A x, where a tile's
-  // x and A are few bytes for one CU, which gets some 60 GB/s of them, and workgroups
-  // have a CU each: rank 16, one row of 2048 8.2 us against 9.2 by two, 64 rows of 5
-  // adapters 9.0 against 9.9, 2000 of rank 32 13.9 against 15.7, 4200 by 1024 columns
-  // 19.9 against 16.8; 64 adapters of 5120 x 17408 33 against 18. One row of 5120 takes
-  // 10.1 against 9.4 in a graph, but 10.1 against 12.6 launched from the host, which
-  // more rows do not (64 of 5 adapters 12.7 against 10.2 in a graph). An adapter's
-  // last tile is taken for half full; up to QMM_SAME_ROWS rows the choice is that of
-  // as many tiles as they can have.
+  // One launch, in which every workgroup of a tile takes all of A x for itself, where that
+  // is few bytes for one CU and all workgroups run at once. A CU gets some 115 GB/s of
+  // the lines of x and A (A's by 16 rows: ranks 8 and 16 take the same time, 24 and 32 too).
+  // One launch against two, us, one row of one of 8 adapters, 5120 columns, in a graph of
+  // twelve calls, k 2048, 4096, 5120, 6144, 8192: rank 16 7.0 and 7.8, 8.2 and 7.8, 8.8 and 7.8,
+  // 9.4 and 8.2, 10.6 and 8.3; rank 32 7.4 and 8.2, 9.2 and 8.2, 10.1 and 8.2, 10.9 and 8.6, 12.5 and 8.7.
+  // Launched from the host one takes 10.1 and two 12.8, whatever k up to 5120.
+  // So up to QMM_SAME_ROWS rows, a decode step, which is launched either way, one launch goes
+  // on to 340 KiB, where a graph loses 1 us (16 rows of 16 adapters 1.8) and the host
+  // saves 2.7. More rows go by the graph: 64 of 5 adapters, 5120 columns, rank 16, k 2048 8.0
+  // and 8.4, 4096 10.3 and 8.5; 300 of 2048 columns 8.9 and 9.2, 10.9 and 9.8; 1000 of 1024
+  // 9.7 and 11.0, 11.3 and 12.1.
+  // More workgroups than CUs run in two rounds (64 rows of 64 adapters each once, rank 16, k
+  // 2048: 256 workgroups 8.8 and 11.1, 320 14.2 and 11.7). How many have rows only the device knows:
+  // an adapter's last tile is taken for half full (64 rows of 64 adapters drawn at random,
+  // 5120 columns: 340 could be, 200 are, 8.5 and 11.1), and up to QMM_SAME_ROWS rows, where the
+  // choice must not go by them, 14 tiles are taken: with 17408 columns 16 rows of an adapter
+  // each lose (13.9 and 11.2), 12 gain (7.5 and 10.3).
   p.tile = 16;
   p.columns = 1024;
   const bool few = rows <= QMM_SAME_ROWS;
-  const int all = few ? 17 : rows / 16 + (lora_tiles(rows, n_adapters, 16) - rows / 16) / 2;
-  if (rank <= 32 && (16 + rank) * (int64_t)k * 2 <= (few ? 320 << 10 : 192 << 10) &&
-      all * (int64_t)ceil_div(n, p.columns) <= (few ? 320 : 256))
+  const int some16 = few ? 14 : rows / 16 + (lora_tiles(rows, n_adapters, 16) - rows / 16) / 2;
+  if (rank <= 32 && (16 + ceil_div(rank, 16) * 16) * (int64_t)k * 2 <= (few ? 340 << 10 : 192 << 10) &&
+      some16 * (int64_t)ceil_div(n, p.columns) <= kCus)
     return p;
   // Long runs take tiles of 32 rows, which read A and B half as often: 8192 rows
   // of 5 adapters of 5120 x 5120, rank 64: 67 us against 90; 205 rows of each 22
@@ -92,13 +102,13 @@ inline LoraPlan lora_plan(int rows, int n, int k, int rank, int n_adapters, int 
   // Ten blocks of k a part, for four waves: one row of 5120 in 8 parts 9.1 us, in
   // 4 9.4, in 16 9.3; 64 rows of 17408 in 16 parts 14.4, in 8 15.7. Fewer where
   // tiles fill the CUs (512 rows of rank 128: 4 parts 28.7, 8 33.7).
-  p.splits = blocks / 10 < ceil_div(256, tiles) ? blocks / 10 : ceil_div(256, tiles);
+  p.splits = blocks / 10 < ceil_div(kCus, tiles) ? blocks / 10 : ceil_div(kCus, tiles);
   p.splits = p.splits < 1 ? 1 : p.splits > 16 ? 16 : p.splits;
   // One more where that takes a fifth off the CU with the most: of 4096 rows of 5
   // adapters, rank 64, some 130 tiles, 3 parts 40.0 us, 2 42.7, 1 46.2, 4 41.1; of 3000
   // 4 parts 37.2, 3 39.4. An adapter's last tile is taken for half full.
   const int some = rows / p.tile + (tiles - rows / p.tile) / 2, more = p.splits + 1;
-  const int64_t most_now = ceil_div((int64_t)some * p.splits, 256), most_then = ceil_div((int64_t)some * more, 256);
+  const int64_t most_now = ceil_div((int64_t)some * p.splits, kCus), most_then = ceil_div((int64_t)some * more, kCus);
   if (rows > QMM_SAME_ROWS && more <= 16 && more <= blocks / 10 && most_then * p.splits * 5 <= most_now * more * 4)
     p.splits = more;
   // As many columns' shares as let all workgroups run at once, but for an eighth:

@@ -163,6 +163,30 @@ def test_lora_workspaces():
     assert {L.qmm_lora_workspace(r, 5120, 5120, 64, e) // r for r in (1, 2, 7, 16) for e in (1, 3, 1024)} == {8 * 256}
 
 
+def test_lora_in_one_launch():
+    def one(rows, n, k, rank, e):
+        return L.qmm_lora_workspace(rows, n, k, rank, e) == 0
+
+    ks, ns = range(8, 9000, 56), (1, 1024, 1025, 5120, 16384, 17408, 18432, 18433, 20480, 1 << 20)
+    # a rank of 8 takes a rank of 16's time, 24 that of 32: as many lines of A are loaded
+    for rows, e in ((1, 8), (16, 16), (64, 5), (64, 64), (1000, 5)):
+        for lower, upper in ((8, 16), (24, 32)):
+            assert [one(rows, 2048, k, lower, e) for k in ks] == [one(rows, 2048, k, upper, e) for k in ks], (rows, lower)
+    # few rows: the choice, and so a row's bits, goes by n, k and rank alone
+    for n in ns:
+        for k in (64, 2048, 3624, 3632, 5120, 5440, 5448, 8192):
+            for rank in (8, 16, 24, 32, 40):
+                assert len({one(rows, n, k, rank, e) for rows in (1, 2, 9, 16) for e in (1, 8, 16, 1024)}) == 1, (n, k, rank)
+    # one launch up to some length, then two; and none above rank 32
+    for rows, e in ((1, 8), (16, 1024), (17, 3), (64, 5), (1000, 5)):
+        for rank in (8, 16, 24, 32):
+            took = [one(rows, 1024, k, rank, e) for k in ks]
+            assert took[0] and not took[-1] and took == sorted(took, reverse=True), (rows, rank)
+        assert not one(rows, 64, 64, 40, e)
+    # more workgroups than CUs would wait for each other
+    assert one(300, 5120, 1024, 16, 5) and not one(2000, 5120, 1024, 16, 5) and not one(100, 5120, 1024, 16, 100)
+
+
 def verify(p=X, qq=Z, ty=F32, tok=IDS, ln=LEN, u=U, acc=DW, out=Y, r=3, d=4, v=20000, ws=TMP, wn=1 << 30):
     return L.qmv_verify_drafts(V(p), V(qq), ty, V(tok), V(ln), V(u), V(acc), V(out), r, d, v, V(ws), wn, None)
 
