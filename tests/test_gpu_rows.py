@@ -413,3 +413,26 @@ def test_refusals_of_the_binding(q, dev):
         q.qmm_rows_combine_grad(f, None, i, dw=torch.zeros((4, 2), device=dev))
     with pytest.raises(q.QmvError):
         q.qmm_rows_combine_grad(f, f.clone(), i, dz=f)
+
+
+def test_the_most_choices_and_the_widest_rows(q, dev):
+    n = 1 << 24
+    ids = choices(rng(12), n // 32, 32, 1024, 0.1)
+    for got, exact in zip(sort_into_guards(q, dev, ids, 1024), np_sort(ids, 1024)):
+        assert np.array_equal(got, exact)
+    h, top_k = 1 << 20, 3
+    places = torch.tensor([[5, 0, -1], [2, 6, 3]], dtype=torch.int32, device=dev)
+    at, held = places.clamp(min=0).long(), (places >= 0).float()
+    w = torch.tensor([[2.0, -1.0, 9.0], [3.0, 0.5, 4.0]], device=dev)
+    for width in (h, h - 3):                                   # whole pieces, and rows that start anywhere
+        x = ((torch.arange(2 * width, device=dev) * 7 % 17).float() - 8).view(2, width)
+        for kind in (torch.float32, torch.bfloat16):
+            z = q.qmm_rows_spread(x.to(kind), places, rows=7)
+            assert torch.equal(z[at] * held[:, :, None].to(kind), x.to(kind)[:, None] * held[:, :, None].to(kind))
+            assert bool((z[[1, 4]] == 0).all())
+            assert torch.equal(q.qmm_rows_combine(z, places, w), x * (w * held).sum(1, keepdim=True))
+            dz, dw = q.qmm_rows_combine_grad(x.to(kind), z, places, w)
+            want = (x[:, None] * (w * held)[:, :, None]).to(kind)
+            assert torch.equal(dz[at] * held[:, :, None].to(kind), want)
+            got = (x.double() ** 2).sum(1, keepdim=True) * held   # whole numbers up to 2^25: the last additions round
+            assert bool(((dw - got).abs() <= 16 * 2.0 ** -24 * got).all())
