@@ -15,15 +15,15 @@
 // what fp32 additions lose.
 //
 // What bounds it. Few rows: a launch and trips to memory one behind the other, the
-// run's offsets, its index, A and x, then B (one row, rank 16, 5120 x 5120: 10 us,
-// launches included; 64 rows of 24 adapters, rank 32, k 5120, 17408 columns: 5.1 and
-// 9.4 us, where a large copy would take 4.6 for the bytes). Long runs: the L2, of which a CU
+// run's offsets, its index, A and x, then B (one row, rank 16, 5120 x 5120: 8.8 us in
+// a graph of many calls, 10.1 launched from the host; 64 rows of 24 adapters, rank 32, k 5120,
+// 17408 columns: 5.1 and 9.4 us, where a large copy would take 4.6 for the bytes). Long runs: the L2, of which a CU
 // gets some 24 bytes a cycle, since each tile of 32 rows reads all of A and B (4096
 // rows of 5 adapters, rank 64, 5120 x 5120, bf16: 13.5 and 24.3 us, 42 MB read and
-// 84 MB read and written, 3.1 and 3.4 TB/s of a large copy's 5.2; the products alone
+// 84 MB read and written, 3.1 and 3.5 TB/s of a large copy's 5.2; the products alone
 // would be 2 and 7 us at a large library product's rate). Both products of 16 rows in
-// one workgroup read A and B twice as often and took 51 us; tiles of 64 rows gained
-// nothing over 32.
+// one workgroup read A and B twice as often and took 51 us; tiles of 64 rows, with
+// A and B through registers as here, gained nothing over 32.
 #include "rows_device.h"
 #include "rows_internal.h"
 #include "rows_layout.h"

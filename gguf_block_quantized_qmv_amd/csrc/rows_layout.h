@@ -139,7 +139,10 @@ inline size_t lora_workspace(int rows, int n, int k, int rank, int n_adapters) {
 constexpr int kVerifyChunk = 1024;   // tokens of one wave: 64 lanes of 16
 
 // A workgroup a request, in one launch and without a workspace, where its 16 waves
-// have a chunk each: 8192 tokens 7.5 us against 9.3 by two launches, 32768 11 and 9.5.
+// have a chunk each. One launch against two, us, fp32, in a graph of twelve calls: one
+// request of 8192 tokens 6.3 and 7.7, 16384 7.5 and 7.9, 24576 8.2 and 7.9, 32768 9.7 and 7.9;
+// 16 of 24576 8.4 and 8.3; 256 of 16384 10.4 and 13.2, of 32768 15.1 and 16.9, 131072 46.0 and
+// 45.4: with a request for each CU the change would come later. A workspace goes by the vocabulary.
 inline bool verify_whole(int vocab) { return vocab <= 16 * kVerifyChunk; }
 
 // Two fp64 sums for each request and chunk.

@@ -121,7 +121,8 @@ size_t qmm_lora_workspace(int rows, int n, int k, int rank, int n_adapters);
  *              as they were in y.
  *   ws         as in qmm_rows_sort, of qmm_lora_workspace(...) bytes
  *   rows >= 0 (0: nothing is done), n >= 1, k >= 8 and k % 8 == 0,
- *   rank >= 8 and rank % 8 == 0, 1 <= n_adapters <= QMM_MAX_EXPERTS
+ *   rank >= 8 and rank % 8 == 0, 1 <= n_adapters <= QMM_MAX_EXPERTS,
+ *   (rows / 16 + min(rows, n_adapters)) * ceil(n / 256) <= 2^28
  * Offsets are clamped to [0, rows]; where they decrease, which rows are written
  * is not defined, but no memory outside the arguments is touched. The order of
  * the sums depends on the sizes alone; for rows <= QMM_SAME_ROWS a row's bits

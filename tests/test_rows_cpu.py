@@ -163,6 +163,13 @@ def test_lora_workspaces():
     assert {L.qmm_lora_workspace(r, 5120, 5120, 64, e) // r for r in (1, 2, 7, 16) for e in (1, 3, 1024)} == {8 * 256}
 
 
+def test_lora_with_more_workgroups_than_a_grid_takes():
+    # (rows / 16 + min(rows, adapters)) * ceil(n / 256) up to 2^28: 65536 tiles by 4096
+    n, rows = 1 << 20, (65536 - 4) * 16
+    assert lora(n=n, rows=rows, ws=0) == WORKSPACE             # in range: the next check speaks
+    assert lora(n=n, rows=rows + 16, ws=0) == RANGE and L.qmm_lora_workspace(rows + 16, n, 256, 40, 4) == 0
+
+
 def test_lora_in_one_launch():
     def one(rows, n, k, rank, e):
         return L.qmm_lora_workspace(rows, n, k, rank, e) == 0
