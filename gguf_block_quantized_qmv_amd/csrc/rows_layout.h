@@ -85,7 +85,7 @@ inline LoraPlan lora_plan(int rows, int n, int k, int rank, int n_adapters, int 
   // an adapter's last tile is taken for half full (64 rows of 64 adapters drawn at random,
   // 5120 columns: 340 could be, 200 are, 8.5 and 11.1), and up to QMM_SAME_ROWS rows, where the
   // choice must not go by them, 14 tiles are taken: with 17408 columns 16 rows of an adapter
-  // each lose (13.9 and 11.2), 12 gain (7.5 and 10.3).
+  // each lose (13.9 and 11.2, at k 5120 18.6 and 11.5), 12 gain (7.5 and 10.3, 9.9 and 10.1).
   p.tile = 16;
   p.columns = 1024;
   const bool few = rows <= QMM_SAME_ROWS;

@@ -189,7 +189,8 @@ __global__ __launch_bounds__(256) void rows_combine_kernel(const MoveArgs p, con
 // products of G choices in registers and add them up at the end, in an order that
 // goes by the width alone; dy is read again for each G of them, once up to top 8.
 // The whole workgroup where a row has more pieces than a wave: 4096 tokens of 2048
-// bf16, top 8, 62 us against a wave's 74. Groups of G choices by top_k as above: 16384 tokens of top 2 54 us, with groups of 8 73.
+// bf16, top 8, 62 us against a wave's 74. Groups of G choices by top_k as above:
+// 16384 tokens of top 2 54 us, with groups of 8 73.
 template <bool F32, int A, int LANES, int G, bool FAR>
 __global__ __launch_bounds__(256) void rows_combine_grad_kernel(const MoveArgs p, const int pieces) {
   constexpr int V = kValues<F32>;
