@@ -736,7 +736,7 @@ def _work_memory(ws, name, sizes, device, index, stream):
         if not need:
             return None, 0, None
         ws = _new((need,), _U8[0], device, stream)
-    have = ws.numel()
+    have, = _sizes(ws, "ws", _U8, 1)
     return _take(ws, "ws", _U8, (have,), index), have, ws
 
 
@@ -840,6 +840,7 @@ def qmm_rows_combine(z, places, weights=None, y=None, out_dtype=None, stream=Non
     _in_c(name, tokens, top_k, h)
     if y is None:
         y = _new((tokens, h), out_dtype or _F32[0], z.device, stream)
+    _sizes(y, "y", _FLOATS, 2)
     y_type = _y_type(y, out_dtype)
     zp, pp, wp, yp = _addresses(index, (z, "z", _FLOATS, (rows, h)), (places, "places", _I32, (tokens, top_k)),
                                 (weights, "weights", _F32, (tokens, top_k)), (y, "y", _FLOATS, (tokens, h)))
@@ -901,7 +902,7 @@ def qmm_lora(x, a, b, offsets, y, row_index=None, scale=None, ranks=None, base=N
     e, rank, _ = _sizes(a, "a", _BF16, 3)
     _, n, _ = _sizes(b, "b", _BF16, 3)
     _sizes(y, "y", _FLOATS, 2)
-    rows = x_rows if row_index is None else row_index.numel()
+    rows = x_rows if row_index is None else _sizes(row_index, "row_index", _I32, 1)[0]
     _in_c(name, rows, e, rank, k, n)
     y_type = _y_type(y, None)
     ap, bp, sp, rp, xp, op, ip, yp = _addresses(

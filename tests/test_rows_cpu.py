@@ -328,6 +328,31 @@ def test_a_workspace_that_the_binding_makes_lives_until_the_call_has_been_made(m
     assert [m() for m in made] == [None] * 3                   # and no longer
 
 
+def test_what_is_no_tensor_is_refused_by_name(monkeypatch):
+    calls = []
+    monkeypatch.setattr(q, "_run", lambda *a: calls.append(a))
+    f, bf = torch.float32, torch.bfloat16
+    lora_args = dict(x=Fake((40, 256), bf), a=Fake((4, 40, 256), bf), b=Fake((4, 200, 40), bf), offsets=Fake((5,)),
+                     y=Fake((40, 200), f), ws=Fake((1 << 20,), torch.uint8))
+    z, places, y = Fake((9, 8), f), Fake((4, 3)), Fake((4, 8), f)
+    for name, call in (("row_index", lambda v: q.qmm_lora(**{**lora_args, "row_index": v})),
+                       ("ws", lambda v: q.qmm_lora(**{**lora_args, "ws": v})),
+                       ("scale", lambda v: q.qmm_lora(**{**lora_args, "scale": v})),
+                       ("base", lambda v: q.qmm_lora(**{**lora_args, "base": v})),
+                       ("y", lambda v: q.qmm_lora(**{**lora_args, "y": v})),
+                       ("y", lambda v: q.qmm_rows_combine(z, places, y=v)),
+                       ("weights", lambda v: q.qmm_rows_combine(z, places, v, y=y)),
+                       ("out", lambda v: q.qmm_rows_spread(y, places, out=v)),
+                       ("dz", lambda v: q.qmm_rows_combine_grad(y, z, places, dz=v, dw=Fake((4, 3), f))),
+                       ("ws", lambda v: q.qmm_rows_sort(Fake((4, 8)), 9, Fake((10,)), Fake((32,)), Fake((4, 8)), ws=v)),
+                       ("ws", lambda v: q.qmv_verify_drafts(Fake((2, 4, 100), f), Fake((2, 3)), Fake((2, 4), f),
+                                                            accepted=Fake((2,)), tokens=Fake((2, 4)), ws=v))):
+        for bad in ([0] * 4, 7):
+            with pytest.raises(TypeError, match=f"{name} must be a torch tensor"):
+                call(bad)
+    assert calls == []
+
+
 # ------------------------------------------------------------------ the oracle
 
 def test_sort_by_hand():
