@@ -623,11 +623,15 @@ def qmm_fp8_workspace(m: int, n: int, k: int, out_dtype=None, fast_sums: bool = 
 
 
 def _y_type(y, out_dtype, fast_sums=False):
-    if y.dtype not in _FLOATS:
-        raise TypeError(f"y has dtype {y.dtype}, expected float32 or bfloat16")
-    if out_dtype is not None and y.dtype != out_dtype:
-        raise TypeError(f"y has dtype {y.dtype}, out_dtype is {out_dtype}")
-    return _type_code(y.dtype, fast_sums)
+    try:
+        dtype = y.dtype
+    except AttributeError:
+        raise TypeError("y must be a torch tensor") from None
+    if dtype not in _FLOATS:
+        raise TypeError(f"y has dtype {dtype}, expected float32 or bfloat16")
+    if out_dtype is not None and dtype != out_dtype:
+        raise TypeError(f"y has dtype {dtype}, out_dtype is {out_dtype}")
+    return _type_code(dtype, fast_sums)
 
 
 def qmm_fp8(w, w_scale, x, x_scale, n: int, k: int, y=None, out_dtype=None, ws=None, stream=None,
@@ -840,7 +844,6 @@ def qmm_rows_combine(z, places, weights=None, y=None, out_dtype=None, stream=Non
     _in_c(name, tokens, top_k, h)
     if y is None:
         y = _new((tokens, h), out_dtype or _F32[0], z.device, stream)
-    _sizes(y, "y", _FLOATS, 2)
     y_type = _y_type(y, out_dtype)
     zp, pp, wp, yp = _addresses(index, (z, "z", _FLOATS, (rows, h)), (places, "places", _I32, (tokens, top_k)),
                                 (weights, "weights", _F32, (tokens, top_k)), (y, "y", _FLOATS, (tokens, h)))
